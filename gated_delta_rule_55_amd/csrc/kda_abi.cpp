@@ -11,6 +11,7 @@
 #include <cstdint>
 
 #include "kda.h"
+#include "kda_check.h"
 #include "kda_conv.h"
 #include "kda_launch.h"
 
@@ -18,38 +19,13 @@ namespace {
 
 thread_local int g_last_hip_error = 0;
 
-int hip_status(hipError_t e) {
-  if (e == hipSuccess) return KDA_OK;
-  g_last_hip_error = (int)e;
-  return KDA_ERR_HIP;
-}
-
-bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p % a) == 0; }
-
-struct Range {
-  uintptr_t lo, hi;  // [lo, hi)
-};
-
-Range range_of(const void* p, int64_t bytes) {
-  const uintptr_t lo = (uintptr_t)p;
-  return Range{lo, lo + (uintptr_t)(bytes > 0 ? bytes : 0)};
-}
-
-bool overlap(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi && a.hi > a.lo && b.hi > b.lo; }
-
-bool supported_d(int d) { return d == 32 || d == 64 || d == 128; }
-
-// State dtype: 0 or fp32, or bf16 with bf16 inputs.  Sets *bf16_state.
-int check_state_dtype(int32_t state_dtype, int32_t dtype, bool* bf16_state) {
-  if (state_dtype == 0 || state_dtype == KDA_DTYPE_F32) {
-    *bf16_state = false;
-    return KDA_OK;
-  }
-  if (state_dtype != KDA_DTYPE_BF16) return KDA_ERR_DTYPE;
-  if (dtype != KDA_DTYPE_BF16) return KDA_ERR_UNSUPPORTED;
-  *bf16_state = true;
-  return KDA_OK;
-}
+using kda::aligned;
+using kda::check_state_dtype;
+using kda::hip_status;
+using kda::overlap;
+using kda::Range;
+using kda::range_of;
+using kda::supported_d;
 
 // Key heads (0 = H, else a divisor of H) and the q/k normalisation flag.
 int check_qk(int32_t n_k_heads, int32_t qk_l2norm, int H, kda::QkArgs* out) {
@@ -283,6 +259,12 @@ int check_conv(const kda_conv_desc* d, bool fwd, kda::ConvArgs* a) {
 }
 
 }  // namespace
+
+int kda::hip_status(hipError_t e) {
+  if (e == hipSuccess) return KDA_OK;
+  g_last_hip_error = (int)e;
+  return KDA_ERR_HIP;
+}
 
 extern "C" {
 

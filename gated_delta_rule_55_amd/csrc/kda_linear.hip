@@ -1,0 +1,569 @@
+// kda_linear.hip -- linear attention with one decay per head over packed
+// sequences (kda_linear_prefill).
+//
+// In chunks of 64 tokens, with G_i the sum of the log-decays of a chunk's
+// tokens up to and with i, G the whole chunk's and S the state before it:
+//     o_i = scale (exp(G_i) S^T q_i + sum_{j <= i} exp(G_i - G_j) (q_i . k_j) v_j)
+//     S  <- exp(G) S + sum_j exp(G - G_j) k_j v_j^T
+// Every factor is at most 1 when g <= 0.  The chunks of a sequence follow one
+// another through S only, and S's decay over any run of tokens is one number,
+// so a sequence longer than a segment of L tokens is split into P segments:
+//     pass 1  every segment but the last: its own state from zero, and its decay
+//     pass 2  S_in of each segment: S_in[p + 1] = decay_p S_in[p] + own_p
+//     pass 3  every segment: its chunks from S_in, writing o; the last one hT
+// A launch in which no sequence can be longer than L runs pass 3 alone.
+//
+// One workgroup walks a segment of one head with the state in registers: wave
+// w owns value columns 32w .. 32w + 31, as dk / 32 D tiles (rows = key
+// channels).  Q, K, V of a chunk lie in LDS; the next chunk's are loaded into
+// registers while it is worked on.  All products are 32x32 MFMA steps:
+//     scores^T = K Q^T     D tiles, decayed and masked, then through LDS as B
+//     O^T      = S^T Q^T   S straight from its registers as A
+//     O^T     += V^T P^T   V read transposed from LDS
+//     S       += K^T V'    V' = exp(G - G_j) v_j
+// V' in bf16 would cost the carried state half its digits, so it is split into
+// three bf16 values (24 bits) and multiplied three times; q's copy of the
+// state and P are rounded to bf16 once, as o will be.
+#include "kda_linear_launch.h"
+#include "kda_linear_ops.h"
+
+namespace kda {
+namespace {
+
+constexpr int C = 64;          // tokens per chunk
+constexpr float kMinG = -200.f;  // exp(-200) is 0 in fp32: -inf becomes a finite sum
+
+struct LinearParams {
+  const void *q, *k, *v;
+  const float* g;
+  void* o;
+  int64_t qs, ks, vs, os;
+  const void* h0;
+  void* ht;
+  const int32_t* cu;
+  const int* slots;
+  float* ws_state;  // [slot][H][dk][dv]
+  float* ws_decay;  // [slot][H] natural log of a segment's decay
+  int64_t T, L;
+  int N, H, rep, n_slots;
+  float scale;
+  bool state_bf16, decay_head;
+};
+
+// Segment `id` of the launch.  Sequence n owns the ids from cu[n] / L + n on:
+// cu[n + 1] / L - cu[n] / L + 1 of them, at least its ceil(len / L) segments.
+struct Segment {
+  int n, p, count;        // sequence, segment in it, its number of segments
+  int64_t begin, end;     // tokens
+  int64_t slot;           // workspace slot of segment 0
+};
+
+__device__ __forceinline__ int64_t cu_at(const LinearParams& P, int n) {
+  if (!P.cu) return n == 0 ? 0 : P.T;
+  const int64_t c = P.cu[n];
+  return c < 0 ? 0 : c > P.T ? P.T : c;
+}
+
+__device__ __forceinline__ Segment sequence_of(const LinearParams& P, int n) {
+  Segment s;
+  s.n = n;
+  s.p = 0;
+  s.begin = cu_at(P, n);
+  const int64_t e = cu_at(P, n + 1);
+  s.end = e > s.begin ? e : s.begin;
+  s.count = (int)((s.end - s.begin + P.L - 1) / P.L);
+  // sequences of two or more segments start in different L-token blocks, with
+  // at least count - 1 blocks to the next such start: twice the block index
+  // leaves room for count slots
+  s.slot = 2 * (s.begin / P.L);
+  return s;
+}
+
+__device__ __forceinline__ bool find_segment(const LinearParams& P, int id, Segment& s) {
+  int lo = 0, hi = P.N - 1;
+  while (lo < hi) {  // the last n with cu[n] / L + n <= id
+    const int mid = (lo + hi + 1) >> 1;
+    if (cu_at(P, mid) / P.L + mid <= id) lo = mid;
+    else hi = mid - 1;
+  }
+  s = sequence_of(P, lo);
+  const int64_t p = id - (s.begin / P.L + lo);
+  if (p < 0 || p >= (s.count > 0 ? s.count : 1)) return false;
+  s.p = (int)p;
+  s.begin += p * P.L;
+  if (s.end > s.begin + P.L) s.end = s.begin + P.L;
+  return true;
+}
+
+// The state slot of sequence n, or -1 to skip it.
+__device__ __forceinline__ int64_t slot_of(const LinearParams& P, int n) {
+  if (!P.slots) return n;
+  const int s = P.slots[n];
+  return s >= 0 && s < P.n_slots ? s : -1;
+}
+
+__device__ __forceinline__ float load_state1(const void* p, int64_t i, bool bf) {
+  return bf ? (float)static_cast<const bf16*>(p)[i] : static_cast<const float*>(p)[i];
+}
+__device__ __forceinline__ void store_state1(void* p, int64_t i, float x, bool bf) {
+  if (bf) static_cast<bf16*>(p)[i] = (bf16)x;
+  else static_cast<float*>(p)[i] = x;
+}
+
+// A chunk's rows of one of q, k, v on their way from memory to LDS: 16-byte
+// vectors, rows past the chunk's end as zeros.
+template <typename T, int D, int NT>
+struct Rows {
+  static constexpr int VE = 16 / sizeof(T);      // elements per vector
+  static constexpr int VPR = D / VE;             // vectors per row
+  static constexpr int RPP = NT / VPR;           // rows per step of the workgroup
+  static constexpr int NV = C / RPP;
+  static constexpr int S = D + 32 / sizeof(T);   // LDS row stride: 32 bytes of padding
+  static_assert(NT % VPR == 0 && C % RPP == 0, "row tiling");
+  uint4 r[NV];
+  // p: this thread's vector of the chunk's first row step
+  __device__ __forceinline__ void load(const T* p, int64_t stride, int valid, int tid) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      r[i] = uint4{0, 0, 0, 0};
+      if (tid / VPR + i * RPP < valid)
+        r[i] = *reinterpret_cast<const uint4*>(p + (int64_t)(i * RPP) * stride);
+    }
+  }
+  __device__ __forceinline__ void store(T* lds, int tid) const {
+    T* p = lds + (tid / VPR) * S + (tid % VPR) * VE;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) *reinterpret_cast<uint4*>(p + i * RPP * S) = r[i];
+  }
+};
+
+// LDS of a workgroup.
+template <typename T, int DK, int DV, bool OUT>
+struct Smem {
+  alignas(16) T k[C * Rows<T, DK, 64>::S];
+  alignas(16) T v[C * Rows<T, DV, 64>::S];
+  alignas(16) T q[OUT ? C * Rows<T, DK, 64>::S : 8];
+  alignas(16) T p[OUT ? 2 : 1][OUT ? 3 * 2 * 64 * 8 : 8];  // score tiles as B operands
+  // per token of the chunk, in powers of two: G as hi + lo, exp(G_i), exp(G - G_i)
+  alignas(16) float ghi[C], glo[C], eg[C], ed[C];
+  float total;  // exp(G)
+};
+
+// One wave: the log-decay sums of a chunk and what is made of them.  Sums are
+// fp64, and differences are taken from hi + lo pairs, so that a strong decay
+// in the chunk does not cost the weaker ones after it their digits.  Returns G.
+template <typename SM>
+__device__ __forceinline__ double decay_sums(SM& sm, float g, bool head, int valid, int lane) {
+  g = g < kMinG ? kMinG : g;
+  double G, all;
+  if (head) {
+    const int n = lane + 1 < valid ? lane + 1 : valid;
+    G = (double)g * n;
+    all = (double)g * valid;
+  } else {
+    G = lane < valid ? (double)g : 0.0;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const double x = __shfl_up(G, off, 64);
+      if (lane >= off) G += x;
+    }
+    all = __shfl(G, 63, 64);
+  }
+  constexpr double kL2E = 1.4426950408889634074;
+  const double G2 = G * kL2E;
+  const float hi = (float)G2;
+  sm.ghi[lane] = hi;
+  sm.glo[lane] = (float)(G2 - (double)hi);
+  sm.eg[lane] = fast_exp2(hi);
+  sm.ed[lane] = fast_exp2((float)((all - G) * kL2E));
+  if (lane == 0) sm.total = fast_exp2((float)(all * kL2E));
+  return all;
+}
+
+// Passes 1 (OUT = false) and 3 (OUT = true).
+template <typename T, int DK, int DV, bool OUT>
+__global__ __launch_bounds__(2 * DV, sizeof(T) == 2 && DV == 128 ? 2 : 1) void linear_kernel(LinearParams P) {
+  constexpr int NW = DV / 32, NT = 64 * NW, KT = DK / 32;
+  using RQ = Rows<T, DK, NT>;
+  using RV = Rows<T, DV, NT>;
+  using F = typename Frag<T>::type;
+  __shared__ Smem<T, DK, DV, OUT> sm;
+
+  const int h = blockIdx.x % P.H;
+  Segment s;
+  if (!find_segment(P, blockIdx.x / P.H, s)) return;
+  if (!OUT && s.p + 1 >= s.count) return;
+  const int64_t slot = slot_of(P, s.n);
+  if (slot < 0) return;
+
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+  const int half = lane >> 5, col = lane & 31;
+  const bool sbf = P.state_bf16;
+  const int64_t sbase = (slot * P.H + h) * (int64_t)(DK * DV);
+  const int64_t wbase = ((s.slot + s.p) * P.H + h) * (int64_t)(DK * DV);
+  // lane's state element of tile t, register r: row 32t + 16 (r / 8) + 8 half + r % 8
+  const int lrow = 8 * half, lcol = 32 * w + col;
+  auto at = [&](int t, int r) { return (32 * t + 16 * (r >> 3) + lrow + (r & 7)) * DV + lcol; };
+
+  f32x16 S[KT];
+#pragma unroll
+  for (int t = 0; t < KT; ++t)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) S[t][r] = 0.f;
+  if (OUT) {
+    if (s.count > 1) {
+#pragma unroll
+      for (int t = 0; t < KT; ++t)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) S[t][r] = P.ws_state[wbase + at(t, r)];
+    } else if (P.h0) {
+#pragma unroll
+      for (int t = 0; t < KT; ++t)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) S[t][r] = load_state1(P.h0, sbase + at(t, r), sbf);
+    }
+  }
+
+  const int hk = h / P.rep;
+  const T* qp = OUT ? static_cast<const T*>(P.q) + (s.begin + tid / RQ::VPR) * P.qs + hk * DK +
+                          (tid % RQ::VPR) * RQ::VE
+                    : nullptr;
+  const T* kp = static_cast<const T*>(P.k) + (s.begin + tid / RQ::VPR) * P.ks + hk * DK +
+                (tid % RQ::VPR) * RQ::VE;
+  const T* vp = static_cast<const T*>(P.v) + (s.begin + tid / RV::VPR) * P.vs + h * DV +
+                (tid % RV::VPR) * RV::VE;
+  RQ rq, rk;
+  RV rv;
+  float g = 0.f;
+  double logsum = 0.0;
+  const bool gwave = w == NW - 1;
+  auto fetch = [&](int64_t t0) {
+    const int64_t left = s.end - t0;
+    const int valid = left < C ? (int)left : C;
+    const int64_t d = t0 - s.begin;
+    if (OUT) rq.load(qp + d * P.qs, P.qs, valid, tid);
+    rk.load(kp + d * P.ks, P.ks, valid, tid);
+    rv.load(vp + d * P.vs, P.vs, valid, tid);
+    if (gwave) g = P.decay_head ? P.g[h] : lane < valid ? P.g[(t0 + lane) * P.H + h] : 0.f;
+  };
+  auto publish = [&](int64_t t0) {
+    const int64_t left = s.end - t0;
+    const int valid = left < C ? (int)left : C;
+    if (OUT) rq.store(sm.q, tid);
+    rk.store(sm.k, tid);
+    rv.store(sm.v, tid);
+    if (gwave) logsum += decay_sums(sm, g, P.decay_head, valid, lane);
+  };
+
+  if (s.begin < s.end) {
+    fetch(s.begin);
+    publish(s.begin);
+  }
+  __syncthreads();
+  int buf = 0;
+  for (int64_t t0 = s.begin; t0 < s.end; t0 += C, buf ^= 1) {
+    const bool more = t0 + C < s.end;
+    if (more) fetch(t0 + C);
+
+    f32x16 O[2];
+    if (OUT) {
+      // scores^T of tile (jt, it): rows = keys j, columns = queries i
+      for (int tile = w; tile < 3; tile += NW) {
+        const int jt = tile >> 1, it = (tile + 1) >> 1;
+        f32x16 a;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) a[r] = 0.f;
+        const T* krow = sm.k + (32 * jt + col) * RQ::S + 8 * half;
+        const T* qrow = sm.q + (32 * it + col) * RQ::S + 8 * half;
+#pragma unroll
+        for (int x = 0; x < DK / 16; ++x) a = mma(load_frag8<T>(krow + 16 * x), load_frag8<T>(qrow + 16 * x), a);
+        const int i = 32 * it + col;
+        const float hi = sm.ghi[i], lo = sm.glo[i];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const int j = 32 * jt + 16 * x + 8 * y + 4 * half;
+            const f32x4 jh = *reinterpret_cast<const f32x4*>(sm.ghi + j);
+            const f32x4 jl = *reinterpret_cast<const f32x4*>(sm.glo + j);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int r = 8 * x + 4 * y + e;
+              const float dec = fast_exp2((hi - jh[e]) + (lo - jl[e]));
+              a[r] = j + e <= i ? a[r] * dec : 0.f;
+            }
+          }
+          store_frag8(sm.p[buf] + ((tile * 2 + x) * 64 + lane) * 8, frag_of_d<T>(a, x));
+        }
+      }
+      // O^T = S^T Q^T, then the decay since the chunk's start
+#pragma unroll
+      for (int it = 0; it < 2; ++it)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) O[it][r] = 0.f;
+#pragma unroll
+      for (int t = 0; t < KT; ++t)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const F sf = frag_of_d<T>(S[t], x);
+#pragma unroll
+          for (int it = 0; it < 2; ++it)
+            O[it] = mma(sf, load_frag8<T>(sm.q + (32 * it + col) * RQ::S + 32 * t + 16 * x + 8 * half), O[it]);
+        }
+#pragma unroll
+      for (int it = 0; it < 2; ++it) {
+        const float e = sm.eg[32 * it + col];
+#pragma unroll
+        for (int r = 0; r < 16; ++r) O[it][r] *= e;
+      }
+    }
+
+    // S = exp(G) S + K^T V'
+    F vf[4];
+    bool bad = false;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      vf[x] = frag_t<false>(sm.v + 16 * x * RV::S + 32 * w, RV::S, lane);
+      bad |= any_nonfinite(vf[x]);
+    }
+    const bool wave_bad = __any(bad);
+    const float total = sm.total;
+#pragma unroll
+    for (int t = 0; t < KT; ++t)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) S[t][r] *= total;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const f32x4 d0 = *reinterpret_cast<const f32x4*>(sm.ed + 16 * x + 4 * half);
+      const f32x4 d1 = *reinterpret_cast<const f32x4*>(sm.ed + 16 * x + 8 + 4 * half);
+      f32x8 vd;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) vd[e] = to_f32(vf[x][e]) * (e < 4 ? d0[e & 3] : d1[e & 3]);
+      if constexpr (sizeof(T) == 2) {
+        bf16x8 va, vb, vc;
+        split3(vd, va, vb, vc);
+        if (wave_bad) {  // what is not finite is not split
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (!finite1(vd[e])) vb[e] = vc[e] = (bf16)0.f;
+        }
+#pragma unroll
+        for (int t = 0; t < KT; ++t) {
+          const F kf = frag_t<true>(sm.k + 16 * x * RQ::S + 32 * t, RQ::S, lane);
+          S[t] = mma(kf, vc, S[t]);
+          S[t] = mma(kf, vb, S[t]);
+          S[t] = mma(kf, va, S[t]);
+        }
+      } else {
+#pragma unroll
+        for (int t = 0; t < KT; ++t)
+          S[t] = mma(frag_t<true>(sm.k + 16 * x * RQ::S + 32 * t, RQ::S, lane), vd, S[t]);
+      }
+    }
+    __syncthreads();  // the scores are written; this chunk's Q, K, V and decays are read
+    if (more) publish(t0 + C);
+
+    if (OUT) {
+      if (wave_bad) {  // a masked score of 0 would turn these into NaN: added below
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (!finite1(to_f32(vf[x][e]))) vf[x][e] = from_f32<T>(0.f);
+      }
+#pragma unroll
+      for (int tile = 0; tile < 3; ++tile) {
+        const int jt = tile >> 1, it = (tile + 1) >> 1;
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+          O[it] = mma(vf[2 * jt + x], load_frag8<T>(sm.p[buf] + ((tile * 2 + x) * 64 + lane) * 8), O[it]);
+      }
+      const int64_t left = s.end - t0;
+      const int valid = left < C ? (int)left : C;
+      if (wave_bad) {
+#pragma unroll 1
+        for (int j = 0; j < valid; ++j) {
+          const T* vrow = static_cast<const T*>(P.v) + (t0 + j) * P.vs + h * DV + 32 * w;
+          const int jt = j >> 5, x = (j >> 4) & 1, jj = j & 15;
+          const int e = (jj & 3) + 4 * (jj >> 3), jlane = 32 * ((jj >> 2) & 1) + col;
+          float pj[2];  // P[i][j] of this lane's two queries, 0 before j
+#pragma unroll
+          for (int it = 0; it < 2; ++it)
+            pj[it] = jt <= it ? to_f32(sm.p[buf][(((jt + it) * 2 + x) * 64 + jlane) * 8 + e]) : 0.f;
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            const float x1 = to_f32(vrow[d_row(r, half)]);
+            if (!finite1(x1)) {
+#pragma unroll
+              for (int it = 0; it < 2; ++it)
+                if (32 * it + col >= j) O[it][r] += pj[it] * x1;
+            }
+          }
+        }
+      }
+      // lane: token 32 it + col, value columns 8 (r / 4) + 4 half + r % 4
+#pragma unroll
+      for (int it = 0; it < 2; ++it) {
+        const int i = 32 * it + col;
+        T* op = static_cast<T*>(P.o) + (t0 + i) * P.os + h * DV + 32 * w;
+        if constexpr (sizeof(T) == 2) {
+          // the halves trade register groups, so that each holds 8 columns in a row
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            typedef bf16 b2 __attribute__((ext_vector_type(2)));
+            unsigned int lo[2], hi[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              lo[e] = __builtin_bit_cast(unsigned int, b2{(bf16)(O[it][8 * y + 2 * e] * P.scale), (bf16)(O[it][8 * y + 2 * e + 1] * P.scale)});
+              hi[e] = __builtin_bit_cast(unsigned int, b2{(bf16)(O[it][8 * y + 4 + 2 * e] * P.scale), (bf16)(O[it][8 * y + 5 + 2 * e] * P.scale)});
+            }
+            const auto s0 = __builtin_amdgcn_permlane32_swap(lo[0], hi[0], false, false);
+            const auto s1 = __builtin_amdgcn_permlane32_swap(lo[1], hi[1], false, false);
+            if (i < valid)
+              *reinterpret_cast<uint4*>(op + 16 * y + 8 * half) = uint4{s0[0], s1[0], s0[1], s1[1]};
+          }
+        } else {
+          if (i < valid) {
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+              *reinterpret_cast<f32x4*>(op + 8 * y + 4 * half) =
+                  f32x4{O[it][4 * y], O[it][4 * y + 1], O[it][4 * y + 2], O[it][4 * y + 3]} * P.scale;
+          }
+        }
+      }
+    }
+    __syncthreads();  // the next chunk is in LDS
+  }
+
+  if (OUT) {
+    if (P.ht && s.p + 1 >= s.count) {
+#pragma unroll
+      for (int t = 0; t < KT; ++t)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) store_state1(P.ht, sbase + at(t, r), S[t][r], sbf);
+    }
+  } else {
+#pragma unroll
+    for (int t = 0; t < KT; ++t)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) P.ws_state[wbase + at(t, r)] = S[t][r];
+    if (gwave && lane == 0) P.ws_decay[(s.slot + s.p) * P.H + h] = (float)logsum;
+  }
+}
+
+// Pass 2: the state each segment of a split sequence starts from, in place of
+// the segments' own states.  A thread walks four elements through the
+// segments; 1 / (dk dv) of the arithmetic, bound by the workspace's traffic.
+__global__ __launch_bounds__(256) void linear_join_kernel(LinearParams P, int elems, int parts) {
+  const int part = blockIdx.x % parts;
+  const int nh = blockIdx.x / parts;
+  const int h = nh % P.H;
+  const Segment s = sequence_of(P, nh / P.H);
+  if (s.count < 2) return;
+  const int64_t slot = slot_of(P, s.n);
+  if (slot < 0) return;
+  const int e = (part * 256 + threadIdx.x) * 4;
+  if (e >= elems) return;
+  f32x4 S = f32x4{0.f, 0.f, 0.f, 0.f};
+  if (P.h0) {
+    const int64_t b = (slot * P.H + h) * (int64_t)elems + e;
+    S = P.state_bf16 ? load_state4(static_cast<const bf16*>(P.h0) + b)
+                     : load_state4(static_cast<const float*>(P.h0) + b);
+  }
+  const int64_t step = (int64_t)P.H * elems;
+  float* p = P.ws_state + (s.slot * P.H + h) * (int64_t)elems + e;
+  const float* d = P.ws_decay + s.slot * P.H + h;
+  for (int i = 0; i < s.count; ++i, p += step, d += P.H) {
+    const bool last = i + 1 == s.count;
+    f32x4 own = last ? S : *reinterpret_cast<const f32x4*>(p);
+    *reinterpret_cast<f32x4*>(p) = S;
+    if (!last) S = S * fast_exp2(*d * kLog2e) + own;
+  }
+}
+
+template <typename T, int DK, int DV>
+hipError_t launch(const LinearParams& p, bool split, hipStream_t stream) {
+  const int64_t blocks = linear_segments(p.T, p.N, p.L) * p.H;
+  if (split) {
+    linear_kernel<T, DK, DV, false><<<(unsigned)blocks, 2 * DV, 0, stream>>>(p);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    const int parts = DK * DV / 1024;
+    linear_join_kernel<<<(unsigned)((int64_t)p.N * p.H * parts), 256, 0, stream>>>(p, DK * DV, parts);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  linear_kernel<T, DK, DV, true><<<(unsigned)blocks, 2 * DV, 0, stream>>>(p);
+  return hipGetLastError();
+}
+
+template <typename T>
+hipError_t launch_dims(const LinearParams& p, int dk, int dv, bool split, hipStream_t s) {
+  switch (dk * 1000 + dv) {
+    case 32032: return launch<T, 32, 32>(p, split, s);
+    case 32064: return launch<T, 32, 64>(p, split, s);
+    case 32128: return launch<T, 32, 128>(p, split, s);
+    case 64032: return launch<T, 64, 32>(p, split, s);
+    case 64064: return launch<T, 64, 64>(p, split, s);
+    case 64128: return launch<T, 64, 128>(p, split, s);
+    case 128032: return launch<T, 128, 32>(p, split, s);
+    case 128064: return launch<T, 128, 64>(p, split, s);
+    case 128128: return launch<T, 128, 128>(p, split, s);
+    default: return hipErrorInvalidValue;
+  }
+}
+
+size_t decay_bytes(int64_t slots, int H) { return ((size_t)slots * H * 4 + 255) / 256 * 256; }
+int64_t ws_slots(int64_t T, int64_t L) { return 2 * (T / L) + 1; }
+
+}  // namespace
+
+int64_t linear_segment(int64_t t_total, int n_seqs, int n_heads) {
+  (void)n_seqs;
+  // about two workgroups for each of the 256 CUs
+  const int64_t want = (t_total * n_heads + 511) / 512;
+  const int64_t seg = (want + C - 1) / C * C;
+  return seg < 256 ? 256 : seg;
+}
+
+size_t linear_workspace_bytes(const LinearPrefillArgs& a) {
+  const int64_t L = linear_segment(a.t_total, a.n_seqs, a.n_heads);
+  if (a.t_total <= L) return 0;
+  const int64_t slots = ws_slots(a.t_total, L);
+  return decay_bytes(slots, a.n_heads) + (size_t)slots * a.n_heads * a.dk * a.dv * 4;
+}
+
+hipError_t launch_linear_prefill(const LinearPrefillArgs& a, void* workspace, hipStream_t stream) {
+  LinearParams p;
+  p.q = a.q;
+  p.k = a.k;
+  p.v = a.v;
+  p.g = a.g;
+  p.o = a.o;
+  p.qs = a.q_stride;
+  p.ks = a.k_stride;
+  p.vs = a.v_stride;
+  p.os = a.o_stride;
+  p.h0 = a.h0;
+  p.ht = a.ht;
+  p.cu = a.cu_seqlens;
+  p.slots = a.slots;
+  p.T = a.t_total;
+  p.L = linear_segment(a.t_total, a.n_seqs, a.n_heads);
+  p.N = a.n_seqs;
+  p.H = a.n_heads;
+  p.rep = a.n_heads / a.kheads;
+  p.n_slots = a.n_slots;
+  p.scale = a.scale;
+  p.state_bf16 = a.state_bf16;
+  p.decay_head = a.decay_head;
+  const bool split = a.t_total > p.L;
+  p.ws_decay = static_cast<float*>(workspace);
+  p.ws_state = split ? reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) +
+                                                decay_bytes(ws_slots(p.T, p.L), p.H))
+                     : nullptr;
+  return a.bf16 ? launch_dims<bf16>(p, a.dk, a.dv, split, stream)
+                : launch_dims<float>(p, a.dk, a.dv, split, stream);
+}
+
+}  // namespace kda

@@ -10,6 +10,8 @@ it.  Contents:
   gate.py                       the Kimi gate activation (fp64)
   conv.py                       short causal conv with carried taps (fp64)
   heads.py                      q/k L2 normalisation, grouped key heads (fp64)
+  linear.py                     linear attention with a decay per head (fp64)
+  norm.py                       gated and block norms (fp64)
 """
 from .recurrent import (OracleLib, decode, lib_path, num_threads, prefill,  # noqa: F401
                         prefill_f32, set_num_threads)
@@ -17,3 +19,5 @@ from .chunked import chunked_prefill, unit_lower_inverse  # noqa: F401
 from .gate import kimi_gate, softplus  # noqa: F401
 from .conv import causal_conv1d, silu  # noqa: F401
 from .heads import L2NORM_EPS, expand_key_heads, l2norm  # noqa: F401
+from .linear import linear_attention, linear_decode  # noqa: F401
+from .norm import block_norm, gated_norm, rmsnorm  # noqa: F401
