@@ -110,8 +110,10 @@ __device__ __forceinline__ void store_state1(void* p, int64_t i, float x, bool b
   else static_cast<float*>(p)[i] = x;
 }
 
-// A chunk's rows of one of q, k, v on their way from memory to LDS: 16-byte
-// vectors, rows past the chunk's end as zeros.
+// A chunk's rows of one of q, k, v on their way from memory to LDS, as 16-byte
+// vectors.  Loads go through a buffer resource that ends with the chunk's last
+// row, so rows past it read as zeros without a branch, and a thread's offsets
+// are the same for every chunk.
 template <typename T, int D, int NT>
 struct Rows {
   static constexpr int VE = 16 / sizeof(T);      // elements per vector
@@ -121,14 +123,15 @@ struct Rows {
   static constexpr int S = D + 32 / sizeof(T);   // LDS row stride: 32 bytes of padding
   static_assert(NT % VPR == 0 && C % RPP == 0, "row tiling");
   uint4 r[NV];
-  // p: this thread's vector of the chunk's first row step
-  __device__ __forceinline__ void load(const T* p, int64_t stride, int valid, int tid) {
+  static __device__ __forceinline__ int offset(int tid, int64_t stride) {
+    return ((tid / VPR) * (int)stride + (tid % VPR) * VE) * (int)sizeof(T);
+  }
+  // base: the chunk's first row; off: offset() of this thread
+  __device__ __forceinline__ void load(const T* base, int off, int stride, int valid) {
+    const __amdgpu_buffer_rsrc_t rs = make_rsrc(const_cast<T*>(base), ((valid - 1) * stride + D) * (int)sizeof(T));
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      r[i] = uint4{0, 0, 0, 0};
-      if (tid / VPR + i * RPP < valid)
-        r[i] = *reinterpret_cast<const uint4*>(p + (int64_t)(i * RPP) * stride);
-    }
+    for (int i = 0; i < NV; ++i)
+      r[i] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(rs, off + i * RPP * stride * (int)sizeof(T), 0, 0));
   }
   __device__ __forceinline__ void store(T* lds, int tid) const {
     T* p = lds + (tid / VPR) * S + (tid % VPR) * VE;
@@ -137,23 +140,27 @@ struct Rows {
   }
 };
 
-// LDS of a workgroup.
-template <typename T, int DK, int DV, bool OUT>
+// The decays of a chunk's tokens for one head, in powers of two.
+struct Decays {
+  alignas(16) float ghi[C], glo[C];  // G_i as a sum of two floats
+  alignas(16) float eg[C], ed[C];    // exp(G_i), exp(G - G_i)
+  float total;                       // exp(G)
+};
+
+// LDS of a workgroup: VW value columns (HG heads of VW / HG).
+template <typename T, int DK, int VW, int HG, bool OUT>
 struct Smem {
   alignas(16) T k[C * Rows<T, DK, 64>::S];
-  alignas(16) T v[C * Rows<T, DV, 64>::S];
+  alignas(16) T v[C * Rows<T, VW, 64>::S];
   alignas(16) T q[OUT ? C * Rows<T, DK, 64>::S : 8];
-  alignas(16) T p[OUT ? 2 : 1][OUT ? 3 * 2 * 64 * 8 : 8];  // score tiles as B operands
-  // per token of the chunk, in powers of two: G as hi + lo, exp(G_i), exp(G - G_i)
-  alignas(16) float ghi[C], glo[C], eg[C], ed[C];
-  float total;  // exp(G)
+  alignas(16) T p[OUT ? HG * 3 * 2 * 64 * 8 : 8];  // score tiles as B operands
+  Decays d[2][HG];                                 // of this chunk and the next
 };
 
 // One wave: the log-decay sums of a chunk and what is made of them.  Sums are
 // fp64, and differences are taken from hi + lo pairs, so that a strong decay
 // in the chunk does not cost the weaker ones after it their digits.  Returns G.
-template <typename SM>
-__device__ __forceinline__ double decay_sums(SM& sm, float g, bool head, int valid, int lane) {
+__device__ __forceinline__ double decay_sums(Decays& d, float g, bool head, int valid, int lane) {
   g = g < kMinG ? kMinG : g;
   double G, all;
   if (head) {
@@ -172,37 +179,40 @@ __device__ __forceinline__ double decay_sums(SM& sm, float g, bool head, int val
   constexpr double kL2E = 1.4426950408889634074;
   const double G2 = G * kL2E;
   const float hi = (float)G2;
-  sm.ghi[lane] = hi;
-  sm.glo[lane] = (float)(G2 - (double)hi);
-  sm.eg[lane] = fast_exp2(hi);
-  sm.ed[lane] = fast_exp2((float)((all - G) * kL2E));
-  if (lane == 0) sm.total = fast_exp2((float)(all * kL2E));
+  d.ghi[lane] = hi;
+  d.glo[lane] = (float)(G2 - (double)hi);
+  d.eg[lane] = fast_exp2(hi);
+  d.ed[lane] = fast_exp2((float)((all - G) * kL2E));
+  if (lane == 0) d.total = fast_exp2((float)(all * kL2E));
   return all;
 }
 
-// Passes 1 (OUT = false) and 3 (OUT = true).
-template <typename T, int DK, int DV, bool OUT>
-__global__ __launch_bounds__(2 * DV, sizeof(T) == 2 && DV == 128 ? 2 : 1) void linear_kernel(LinearParams P) {
-  constexpr int NW = DV / 32, NT = 64 * NW, KT = DK / 32;
+// Passes 1 (OUT = false) and 3 (OUT = true).  A workgroup walks one segment
+// for HG heads that share a key head: VW value columns in all, 32 a wave.
+template <typename T, int DK, int VW, int HG, bool OUT>
+__global__ __launch_bounds__(2 * VW, sizeof(T) == 2 && VW == 128 && HG < 4 ? 2 : 1) void linear_kernel(LinearParams P) {
+  constexpr int NW = VW / 32, NT = 64 * NW, KT = DK / 32, DV = VW / HG;
   using RQ = Rows<T, DK, NT>;
-  using RV = Rows<T, DV, NT>;
+  using RV = Rows<T, VW, NT>;
   using F = typename Frag<T>::type;
-  __shared__ Smem<T, DK, DV, OUT> sm;
+  __shared__ Smem<T, DK, VW, HG, OUT> sm;
 
-  const int h = blockIdx.x % P.H;
+  const int groups = P.H / HG;
+  const int hb = blockIdx.x % groups * HG;  // first head
   Segment s;
-  if (!find_segment(P, blockIdx.x / P.H, s)) return;
+  if (!find_segment(P, blockIdx.x / groups, s)) return;
   if (!OUT && s.p + 1 >= s.count) return;
   const int64_t slot = slot_of(P, s.n);
   if (slot < 0) return;
 
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
   const int half = lane >> 5, col = lane & 31;
+  const int hw = 32 * w / DV;  // this wave's head of the group
   const bool sbf = P.state_bf16;
-  const int64_t sbase = (slot * P.H + h) * (int64_t)(DK * DV);
-  const int64_t wbase = ((s.slot + s.p) * P.H + h) * (int64_t)(DK * DV);
+  const int64_t sbase = (slot * P.H + hb + hw) * (int64_t)(DK * DV);
+  const int64_t wbase = ((s.slot + s.p) * P.H + hb + hw) * (int64_t)(DK * DV);
   // lane's state element of tile t, register r: row 32t + 16 (r / 8) + 8 half + r % 8
-  const int lrow = 8 * half, lcol = 32 * w + col;
+  const int lrow = 8 * half, lcol = 32 * w % DV + col;
   auto at = [&](int t, int r) { return (32 * t + 16 * (r >> 3) + lrow + (r & 7)) * DV + lcol; };
 
   f32x16 S[KT];
@@ -224,51 +234,72 @@ __global__ __launch_bounds__(2 * DV, sizeof(T) == 2 && DV == 128 ? 2 : 1) void l
     }
   }
 
-  const int hk = h / P.rep;
-  const T* qp = OUT ? static_cast<const T*>(P.q) + (s.begin + tid / RQ::VPR) * P.qs + hk * DK +
-                          (tid % RQ::VPR) * RQ::VE
-                    : nullptr;
-  const T* kp = static_cast<const T*>(P.k) + (s.begin + tid / RQ::VPR) * P.ks + hk * DK +
-                (tid % RQ::VPR) * RQ::VE;
-  const T* vp = static_cast<const T*>(P.v) + (s.begin + tid / RV::VPR) * P.vs + h * DV +
-                (tid % RV::VPR) * RV::VE;
+  const int hk = hb / P.rep;
+  const T* qb = OUT ? static_cast<const T*>(P.q) + s.begin * P.qs + hk * DK : nullptr;
+  const T* kb = static_cast<const T*>(P.k) + s.begin * P.ks + hk * DK;
+  const T* vb = static_cast<const T*>(P.v) + s.begin * P.vs + hb * DV;
+  const int qo = OUT ? RQ::offset(tid, P.qs) : 0, ko = RQ::offset(tid, P.ks), vo = RV::offset(tid, P.vs);
   RQ rq, rk;
   RV rv;
-  float g = 0.f;
-  double logsum = 0.0;
-  const bool gwave = w == NW - 1;
-  auto fetch = [&](int64_t t0) {
-    const int64_t left = s.end - t0;
-    const int valid = left < C ? (int)left : C;
-    const int64_t d = t0 - s.begin;
-    if (OUT) rq.load(qp + d * P.qs, P.qs, valid, tid);
-    rk.load(kp + d * P.ks, P.ks, valid, tid);
-    rv.load(vp + d * P.vs, P.vs, valid, tid);
-    if (gwave) g = P.decay_head ? P.g[h] : lane < valid ? P.g[(t0 + lane) * P.H + h] : 0.f;
+  const int len = (int)(s.end - s.begin);
+  auto valid_at = [&](int c0) { return len - c0 < C ? len - c0 : C; };
+  auto fetch = [&](int c0) {
+    const int valid = valid_at(c0);
+    if (OUT) rq.load(qb + c0 * P.qs, qo, (int)P.qs, valid);
+    rk.load(kb + c0 * P.ks, ko, (int)P.ks, valid);
+    rv.load(vb + c0 * P.vs, vo, (int)P.vs, valid);
   };
-  auto publish = [&](int64_t t0) {
-    const int64_t left = s.end - t0;
-    const int valid = left < C ? (int)left : C;
+  auto publish = [&]() {
     if (OUT) rq.store(sm.q, tid);
     rk.store(sm.k, tid);
     rv.store(sm.v, tid);
-    if (gwave) logsum += decay_sums(sm, g, P.decay_head, valid, lane);
+  };
+  // the last wave, which has no score tile of its own when there are four,
+  // holds the next chunk's log-decays and sums them a chunk ahead
+  const bool gwave = w == NW - 1;
+  float g[HG];
+  double logsum[HG];
+#pragma unroll
+  for (int x = 0; x < HG; ++x) logsum[x] = 0.0;
+  auto fetch_g = [&](int c0) {
+#pragma unroll
+    for (int x = 0; x < HG; ++x)
+      g[x] = P.decay_head ? P.g[hb + x] : lane < len - c0 ? P.g[(s.begin + c0 + lane) * P.H + hb + x] : 0.f;
+  };
+  auto sum_g = [&](int c0, int b) {
+#pragma unroll
+    for (int x = 0; x < HG; ++x) logsum[x] += decay_sums(sm.d[b][x], g[x], P.decay_head, valid_at(c0), lane);
   };
 
-  if (s.begin < s.end) {
-    fetch(s.begin);
-    publish(s.begin);
+  if (len > 0) {
+    fetch(0);
+    if (gwave) {
+      fetch_g(0);
+      sum_g(0, 0);
+      fetch_g(C);
+    }
+    publish();
   }
   __syncthreads();
   int buf = 0;
-  for (int64_t t0 = s.begin; t0 < s.end; t0 += C, buf ^= 1) {
-    const bool more = t0 + C < s.end;
-    if (more) fetch(t0 + C);
+  for (int c0 = 0; c0 < len; c0 += C, buf ^= 1) {
+    const bool more = c0 + C < len;
+    if (more) {
+      fetch(c0 + C);
+      if (gwave) {
+        sum_g(c0 + C, buf ^ 1);
+        fetch_g(c0 + 2 * C);
+      }
+    }
+    const Decays& dw = sm.d[buf][hw];
 
     f32x16 O[2];
     if (OUT) {
       // scores^T of tile (jt, it): rows = keys j, columns = queries i
-      for (int tile = w; tile < 3; tile += NW) {
+#pragma unroll
+      for (int tt = 0; tt < (3 + NW - 1) / NW; ++tt) {
+        const int tile = w + tt * NW;
+        if (tile >= 3) break;
         const int jt = tile >> 1, it = (tile + 1) >> 1;
         f32x16 a;
 #pragma unroll
@@ -278,25 +309,28 @@ __global__ __launch_bounds__(2 * DV, sizeof(T) == 2 && DV == 128 ? 2 : 1) void l
 #pragma unroll
         for (int x = 0; x < DK / 16; ++x) a = mma(load_frag8<T>(krow + 16 * x), load_frag8<T>(qrow + 16 * x), a);
         const int i = 32 * it + col;
-        const float hi = sm.ghi[i], lo = sm.glo[i];
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
+        for (int hx = 0; hx < HG; ++hx) {
+          const Decays& d = sm.d[buf][hx];
+          const float hi = d.ghi[i], lo = d.glo[i];
+          f32x16 b;
 #pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            const int j = 32 * jt + 16 * x + 8 * y + 4 * half;
-            const f32x4 jh = *reinterpret_cast<const f32x4*>(sm.ghi + j);
-            const f32x4 jl = *reinterpret_cast<const f32x4*>(sm.glo + j);
+          for (int x = 0; x < 4; ++x) {
+            const int j = 32 * jt + 8 * x + 4 * half;
+            const f32x4 jh = *reinterpret_cast<const f32x4*>(d.ghi + j);
+            const f32x4 jl = *reinterpret_cast<const f32x4*>(d.glo + j);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const int r = 8 * x + 4 * y + e;
-              const float dec = fast_exp2((hi - jh[e]) + (lo - jl[e]));
-              a[r] = j + e <= i ? a[r] * dec : 0.f;
+              const float dec = fast_exp2((hi - jh[e]) + (lo - jl[e])) * P.scale;
+              b[4 * x + e] = j + e <= i ? a[4 * x + e] * dec : 0.f;
             }
           }
-          store_frag8(sm.p[buf] + ((tile * 2 + x) * 64 + lane) * 8, frag_of_d<T>(a, x));
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+            store_frag8(sm.p + ((hx * 6 + tile * 2 + x) * 64 + lane) * 8, frag_of_d<T>(b, x));
         }
       }
-      // O^T = S^T Q^T, then the decay since the chunk's start
+      // O^T = S^T Q^T, then the decay since the chunk's start and the scale
 #pragma unroll
       for (int it = 0; it < 2; ++it)
 #pragma unroll
@@ -312,7 +346,7 @@ __global__ __launch_bounds__(2 * DV, sizeof(T) == 2 && DV == 128 ? 2 : 1) void l
         }
 #pragma unroll
       for (int it = 0; it < 2; ++it) {
-        const float e = sm.eg[32 * it + col];
+        const float e = dw.eg[32 * it + col] * P.scale;
 #pragma unroll
         for (int r = 0; r < 16; ++r) O[it][r] *= e;
       }
@@ -320,38 +354,29 @@ __global__ __launch_bounds__(2 * DV, sizeof(T) == 2 && DV == 128 ? 2 : 1) void l
 
     // S = exp(G) S + K^T V'
     F vf[4];
-    bool bad = false;
-#pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      vf[x] = frag_t<false>(sm.v + 16 * x * RV::S + 32 * w, RV::S, lane);
-      bad |= any_nonfinite(vf[x]);
-    }
-    const bool wave_bad = __any(bad);
-    const float total = sm.total;
+    float poison = 0.f;  // NaN where a value is not finite
+    const float total = dw.total;
 #pragma unroll
     for (int t = 0; t < KT; ++t)
 #pragma unroll
       for (int r = 0; r < 16; ++r) S[t][r] *= total;
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
-      const f32x4 d0 = *reinterpret_cast<const f32x4*>(sm.ed + 16 * x + 4 * half);
-      const f32x4 d1 = *reinterpret_cast<const f32x4*>(sm.ed + 16 * x + 8 + 4 * half);
+      vf[x] = frag_t<false>(sm.v + 16 * x * RV::S + 32 * w, RV::S, lane);
+      poison = add_nonfinite(vf[x], poison);
+      const f32x4 d0 = *reinterpret_cast<const f32x4*>(dw.ed + 16 * x + 4 * half);
+      const f32x4 d1 = *reinterpret_cast<const f32x4*>(dw.ed + 16 * x + 8 + 4 * half);
       f32x8 vd;
 #pragma unroll
       for (int e = 0; e < 8; ++e) vd[e] = to_f32(vf[x][e]) * (e < 4 ? d0[e & 3] : d1[e & 3]);
       if constexpr (sizeof(T) == 2) {
-        bf16x8 va, vb, vc;
-        split3(vd, va, vb, vc);
-        if (wave_bad) {  // what is not finite is not split
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (!finite1(vd[e])) vb[e] = vc[e] = (bf16)0.f;
-        }
+        bf16x8 va, vb2, vc;
+        split3(vd, va, vb2, vc);
 #pragma unroll
         for (int t = 0; t < KT; ++t) {
           const F kf = frag_t<true>(sm.k + 16 * x * RQ::S + 32 * t, RQ::S, lane);
           S[t] = mma(kf, vc, S[t]);
-          S[t] = mma(kf, vb, S[t]);
+          S[t] = mma(kf, vb2, S[t]);
           S[t] = mma(kf, va, S[t]);
         }
       } else {
@@ -361,35 +386,36 @@ __global__ __launch_bounds__(2 * DV, sizeof(T) == 2 && DV == 128 ? 2 : 1) void l
       }
     }
     __syncthreads();  // the scores are written; this chunk's Q, K, V and decays are read
-    if (more) publish(t0 + C);
+    if (more) publish();
 
     if (OUT) {
-      if (wave_bad) {  // a masked score of 0 would turn these into NaN: added below
+      const bool bad = __any(poison != 0.f);
+      if (bad) {  // a masked score of 0 would turn these into NaN: added below
 #pragma unroll
         for (int x = 0; x < 4; ++x)
 #pragma unroll
           for (int e = 0; e < 8; ++e)
             if (!finite1(to_f32(vf[x][e]))) vf[x][e] = from_f32<T>(0.f);
       }
+      const T* pw = sm.p + hw * 6 * 64 * 8;
 #pragma unroll
       for (int tile = 0; tile < 3; ++tile) {
         const int jt = tile >> 1, it = (tile + 1) >> 1;
 #pragma unroll
         for (int x = 0; x < 2; ++x)
-          O[it] = mma(vf[2 * jt + x], load_frag8<T>(sm.p[buf] + ((tile * 2 + x) * 64 + lane) * 8), O[it]);
+          O[it] = mma(vf[2 * jt + x], load_frag8<T>(pw + ((tile * 2 + x) * 64 + lane) * 8), O[it]);
       }
-      const int64_t left = s.end - t0;
-      const int valid = left < C ? (int)left : C;
-      if (wave_bad) {
+      const int valid = valid_at(c0);
+      if (bad) {
 #pragma unroll 1
         for (int j = 0; j < valid; ++j) {
-          const T* vrow = static_cast<const T*>(P.v) + (t0 + j) * P.vs + h * DV + 32 * w;
+          const T* vrow = vb + (int64_t)(c0 + j) * P.vs + 32 * w;
           const int jt = j >> 5, x = (j >> 4) & 1, jj = j & 15;
           const int e = (jj & 3) + 4 * (jj >> 3), jlane = 32 * ((jj >> 2) & 1) + col;
-          float pj[2];  // P[i][j] of this lane's two queries, 0 before j
+          float pj[2];  // P[i][j] of this lane's two queries
 #pragma unroll
           for (int it = 0; it < 2; ++it)
-            pj[it] = jt <= it ? to_f32(sm.p[buf][(((jt + it) * 2 + x) * 64 + jlane) * 8 + e]) : 0.f;
+            pj[it] = jt <= it ? to_f32(pw[(((jt + it) * 2 + x) * 64 + jlane) * 8 + e]) : 0.f;
 #pragma unroll
           for (int r = 0; r < 16; ++r) {
             const float x1 = to_f32(vrow[d_row(r, half)]);
@@ -405,7 +431,7 @@ __global__ __launch_bounds__(2 * DV, sizeof(T) == 2 && DV == 128 ? 2 : 1) void l
 #pragma unroll
       for (int it = 0; it < 2; ++it) {
         const int i = 32 * it + col;
-        T* op = static_cast<T*>(P.o) + (t0 + i) * P.os + h * DV + 32 * w;
+        T* op = static_cast<T*>(P.o) + (s.begin + c0 + i) * P.os + hb * DV + 32 * w;
         if constexpr (sizeof(T) == 2) {
           // the halves trade register groups, so that each holds 8 columns in a row
 #pragma unroll
@@ -414,8 +440,8 @@ __global__ __launch_bounds__(2 * DV, sizeof(T) == 2 && DV == 128 ? 2 : 1) void l
             unsigned int lo[2], hi[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              lo[e] = __builtin_bit_cast(unsigned int, b2{(bf16)(O[it][8 * y + 2 * e] * P.scale), (bf16)(O[it][8 * y + 2 * e + 1] * P.scale)});
-              hi[e] = __builtin_bit_cast(unsigned int, b2{(bf16)(O[it][8 * y + 4 + 2 * e] * P.scale), (bf16)(O[it][8 * y + 5 + 2 * e] * P.scale)});
+              lo[e] = __builtin_bit_cast(unsigned int, b2{(bf16)O[it][8 * y + 2 * e], (bf16)O[it][8 * y + 2 * e + 1]});
+              hi[e] = __builtin_bit_cast(unsigned int, b2{(bf16)O[it][8 * y + 4 + 2 * e], (bf16)O[it][8 * y + 5 + 2 * e]});
             }
             const auto s0 = __builtin_amdgcn_permlane32_swap(lo[0], hi[0], false, false);
             const auto s1 = __builtin_amdgcn_permlane32_swap(lo[1], hi[1], false, false);
@@ -427,7 +453,7 @@ __global__ __launch_bounds__(2 * DV, sizeof(T) == 2 && DV == 128 ? 2 : 1) void l
 #pragma unroll
             for (int y = 0; y < 4; ++y)
               *reinterpret_cast<f32x4*>(op + 8 * y + 4 * half) =
-                  f32x4{O[it][4 * y], O[it][4 * y + 1], O[it][4 * y + 2], O[it][4 * y + 3]} * P.scale;
+                  f32x4{O[it][4 * y], O[it][4 * y + 1], O[it][4 * y + 2], O[it][4 * y + 3]};
           }
         }
       }
@@ -447,7 +473,10 @@ __global__ __launch_bounds__(2 * DV, sizeof(T) == 2 && DV == 128 ? 2 : 1) void l
     for (int t = 0; t < KT; ++t)
 #pragma unroll
       for (int r = 0; r < 16; ++r) P.ws_state[wbase + at(t, r)] = S[t][r];
-    if (gwave && lane == 0) P.ws_decay[(s.slot + s.p) * P.H + h] = (float)logsum;
+    if (gwave && lane == 0) {
+#pragma unroll
+      for (int x = 0; x < HG; ++x) P.ws_decay[(s.slot + s.p) * P.H + hb + x] = (float)logsum[x];
+    }
   }
 }
 
@@ -481,11 +510,12 @@ __global__ __launch_bounds__(256) void linear_join_kernel(LinearParams P, int el
   }
 }
 
-template <typename T, int DK, int DV>
+template <typename T, int DK, int DV, int HG>
 hipError_t launch(const LinearParams& p, bool split, hipStream_t stream) {
-  const int64_t blocks = linear_segments(p.T, p.N, p.L) * p.H;
+  const int64_t blocks = linear_segments(p.T, p.N, p.L) * (p.H / HG);
+  constexpr int VW = DV * HG;
   if (split) {
-    linear_kernel<T, DK, DV, false><<<(unsigned)blocks, 2 * DV, 0, stream>>>(p);
+    linear_kernel<T, DK, VW, HG, false><<<(unsigned)blocks, 2 * VW, 0, stream>>>(p);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const int parts = DK * DV / 1024;
@@ -493,22 +523,28 @@ hipError_t launch(const LinearParams& p, bool split, hipStream_t stream) {
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  linear_kernel<T, DK, DV, true><<<(unsigned)blocks, 2 * DV, 0, stream>>>(p);
+  linear_kernel<T, DK, VW, HG, true><<<(unsigned)blocks, 2 * VW, 0, stream>>>(p);
   return hipGetLastError();
+}
+
+// Heads narrower than 128 that share a key head are taken together, four waves
+// to a workgroup: q, k and the scores' products are read and made once for them.
+template <typename T, int DK>
+hipError_t launch_dk(const LinearParams& p, int dv, bool split, hipStream_t s) {
+  switch (dv) {
+    case 32: return p.rep % 4 == 0 ? launch<T, DK, 32, 4>(p, split, s) : launch<T, DK, 32, 1>(p, split, s);
+    case 64: return p.rep % 2 == 0 ? launch<T, DK, 64, 2>(p, split, s) : launch<T, DK, 64, 1>(p, split, s);
+    case 128: return launch<T, DK, 128, 1>(p, split, s);
+    default: return hipErrorInvalidValue;
+  }
 }
 
 template <typename T>
 hipError_t launch_dims(const LinearParams& p, int dk, int dv, bool split, hipStream_t s) {
-  switch (dk * 1000 + dv) {
-    case 32032: return launch<T, 32, 32>(p, split, s);
-    case 32064: return launch<T, 32, 64>(p, split, s);
-    case 32128: return launch<T, 32, 128>(p, split, s);
-    case 64032: return launch<T, 64, 32>(p, split, s);
-    case 64064: return launch<T, 64, 64>(p, split, s);
-    case 64128: return launch<T, 64, 128>(p, split, s);
-    case 128032: return launch<T, 128, 32>(p, split, s);
-    case 128064: return launch<T, 128, 64>(p, split, s);
-    case 128128: return launch<T, 128, 128>(p, split, s);
+  switch (dk) {
+    case 32: return launch_dk<T, 32>(p, dv, split, s);
+    case 64: return launch_dk<T, 64>(p, dv, split, s);
+    case 128: return launch_dk<T, 128>(p, dv, split, s);
     default: return hipErrorInvalidValue;
   }
 }

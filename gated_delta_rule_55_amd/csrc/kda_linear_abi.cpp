@@ -19,6 +19,7 @@ using kda::range_of;
 using kda::row_set;
 using kda::RowSet;
 
+constexpr int64_t kMaxStride = (int64_t)1 << 22;
 // (slot, head) states of a pool: keeps its size in bytes in 64 bits.
 constexpr int64_t kMaxStates = (int64_t)1 << 40;
 
@@ -32,12 +33,13 @@ int check_heads(int32_t n_heads, int32_t n_k_heads, int32_t dk, int32_t dv, int*
 }
 
 // A token stride in elements: 0 = dense; else at least the row, a multiple of
-// 16 bytes, and at most 2^28, which keeps every byte offset in 64 bits.
+// 16 bytes, and at most 2^22, which keeps the byte offsets of a 64-token chunk
+// in 31 bits.
 int check_stride(int64_t stride, int64_t row, int64_t es, int64_t* out) {
-  if (stride != 0 && (stride < row || stride * es % 16 != 0 || stride > ((int64_t)1 << 28)))
+  if (stride != 0 && (stride < row || stride * es % 16 != 0 || stride > kMaxStride))
     return KDA_ERR_SHAPE;
   *out = stride == 0 ? row : stride;
-  return KDA_OK;
+  return *out <= kMaxStride ? KDA_OK : KDA_ERR_SHAPE;
 }
 
 int check_linear(const kda_linear_prefill_desc* d, kda::LinearPrefillArgs* a) {

@@ -16,7 +16,6 @@
 namespace kda {
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
-typedef __bf16 bf16x4_lds __attribute__((ext_vector_type(4)));
 
 // D += A B over 16 contraction indices.  bf16: one instruction; fp32: eight,
 // each pairing index e of both halves.
@@ -74,37 +73,48 @@ __device__ __forceinline__ f32x8 frag_t(const float* tile, int stride, int lane)
   return f;
 }
 
-// x as a sum of three bf16 values, to fp32 precision: each step rounds what
-// the ones before left (8 bits each).  Where x is not finite the first holds
-// it and the others are 0.
+// x as a sum of three bf16 values, exactly (8 + 8 + 8 bits): each takes the
+// upper half of what the ones before left.  (Where x is infinite the others
+// are NaN, and so is the sum.)
 __device__ __forceinline__ void split3(const f32x8& x, bf16x8& a, bf16x8& b, bf16x8& c) {
+  unsigned int u[3][8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    a[e] = (bf16)x[e];
-    const float r = x[e] - (float)a[e];
-    b[e] = (bf16)r;
-    c[e] = (bf16)(r - (float)b[e]);
+    float r = x[e];
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      u[i][e] = __builtin_bit_cast(unsigned int, r);
+      r -= __builtin_bit_cast(float, u[i][e] & 0xffff0000u);
+    }
   }
+  u32x4 p[3];
+#pragma unroll
+  for (int i = 0; i < 3; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) p[i][e] = __builtin_amdgcn_perm(u[i][2 * e + 1], u[i][2 * e], 0x07060302u);
+  a = __builtin_bit_cast(bf16x8, p[0]);
+  b = __builtin_bit_cast(bf16x8, p[1]);
+  c = __builtin_bit_cast(bf16x8, p[2]);
 }
 
-// Whether any of the eight values is not finite (all exponent bits set).
-__device__ __forceinline__ bool any_nonfinite(bf16x8 f) {
-  typedef unsigned int u32x4_ __attribute__((ext_vector_type(4)));
-  const u32x4_ u = __builtin_bit_cast(u32x4_, f);
-  unsigned int m = 0;
+// s, or NaN if any of the eight values is not finite: 0 times it is added.
+__device__ __forceinline__ float add_nonfinite(bf16x8 f, float s) {
+  const u32x4 u = __builtin_bit_cast(u32x4, f);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) m |= (u[i] & 0x7f807f80u) + 0x00800080u;
-  return (m & 0x80008000u) != 0;
+  for (int i = 0; i < 4; ++i) {
+    const unsigned int x = u[i];
+    s = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, x), bf16x2{(bf16)0.f, (bf16)0.f}, s, false);
+  }
+  return s;
+}
+__device__ __forceinline__ float add_nonfinite(f32x8 f, float s) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) s = __builtin_fmaf(f[i], 0.f, s);
+  return s;
 }
 // (By value: a bit cast of a vector's element in place reads element 0.)
 __device__ __forceinline__ bool finite1(float x) {
   return (__builtin_bit_cast(unsigned int, x) & 0x7f800000u) != 0x7f800000u;
-}
-__device__ __forceinline__ bool any_nonfinite(f32x8 f) {
-  bool m = false;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) m |= !finite1(f[i]);
-  return m;
 }
 
 }  // namespace kda

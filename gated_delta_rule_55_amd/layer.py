@@ -29,7 +29,15 @@ def _guard(dev, stream):
                 yield
 
 
-_HERE = contextlib.nullcontext()
+class _Here:
+    def __enter__(self):
+        pass
+
+    def __exit__(self, *exc):
+        pass
+
+
+_HERE = _Here()
 
 
 def _on(dev, stream):
@@ -38,6 +46,17 @@ def _on(dev, stream):
     if stream is None and dev.index == torch.cuda.current_device():
         return _HERE
     return _guard(dev, stream)
+
+
+# The current stream's handle: a torch.cuda.Stream object made for it would cost
+# as much as the rest of a call's checks (2 us).
+_current_handle = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _raw_stream(dev) -> int:
+    if _current_handle is not None:
+        return _current_handle(dev.index)
+    return torch.cuda.current_stream(dev).cuda_stream
 
 
 def _fail(t, name, shape, dtype, dev):
@@ -161,7 +180,7 @@ def linear_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.T
     h0p = None if h0 is None else _dense(h0, "h0", shape, sd, dev)
     with _on(dev, stream):
         if out is None:
-            out = torch.empty((T, H, dv), dtype=dt, device=dev)
+            out = v.new_empty((T, H, dv))
             op, os_ = out.data_ptr(), 0
         else:
             op, os_ = _rows3(out, "out", (T, H, dv), dt, dev)
@@ -185,10 +204,6 @@ def linear_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.T
     if st != _abi.KDA_OK:
         raise _abi.KdaError(st, "kda_linear_prefill")
     return out, ht
-
-
-def _raw_stream(dev) -> int:
-    return torch.cuda.current_stream(dev).cuda_stream
 
 
 def linear_decode(state: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
@@ -220,7 +235,7 @@ def linear_decode(state: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torc
     decay, gp = _decay(g, N, H, dev)
     with _on(dev, stream):
         if out is None:
-            out = torch.empty((N, H, dv), dtype=dt, device=dev)
+            out = v.new_empty((N, H, dv))
             op, os_ = out.data_ptr(), 0
         else:
             op, os_ = _rows3(out, "out", (N, H, dv), dt, dev)
@@ -295,7 +310,7 @@ def gated_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
     zp, zs = (None, 0) if gate is None else _rows(gate, "gate", shape, dt, dev)
     with _on(dev, stream):
         if out is None:
-            out = torch.empty(shape, dtype=dt, device=dev)
+            out = x.new_empty(shape)
             yp, ys = out.data_ptr(), 0
         else:
             yp, ys = _rows(out, "out", shape, dt, dev)
@@ -344,14 +359,14 @@ def block_norm(x: torch.Tensor, residual: torch.Tensor,
         raise ValueError("out needs weight_pre")
     with _on(dev, stream):
         if residual_out is None:
-            residual_out = torch.empty(shape, dtype=rd, device=dev)
+            residual_out = residual.new_empty(shape)
             rop, ros = residual_out.data_ptr(), 0
         else:
             rop, ros = _rows(residual_out, "residual_out", shape, rd, dev)
         yp, ys = None, 0
         if weight_pre is not None:
             if out is None:
-                out = torch.empty(shape, dtype=dt, device=dev)
+                out = x.new_empty(shape)
                 yp = out.data_ptr()
             else:
                 yp, ys = _rows(out, "out", shape, dt, dev)

@@ -21,8 +21,8 @@
  *   - dk and dv are chosen separately, each in {32, 64, 128}.
  *   - q, k, v and o may have a token stride of their own (a slice of a wider
  *     buffer): the number of elements from one token's first to the next
- *     one's, at least heads * head dim, at most 2^28 and a multiple of 16
- *     bytes; 0 = dense.
+ *     one's, at least heads * head dim, a multiple of 16 bytes; 0 = dense.
+ *     Dense or not, it is at most 2^22.
  *   - Alignment: 16 bytes for q, k, v, o, h0, ht and the decode state; g and
  *     the index tables, 4 bytes.
  *
