@@ -102,12 +102,23 @@ __device__ __forceinline__ int64_t slot_of(const LinearParams& P, int n) {
   return s >= 0 && s < P.n_slots ? s : -1;
 }
 
-__device__ __forceinline__ float load_state1(const void* p, int64_t i, bool bf) {
-  return bf ? (float)static_cast<const bf16*>(p)[i] : static_cast<const float*>(p)[i];
+// A wave's part of a state in memory, [DK][DV] at p of type TS, to or from its
+// D tiles: register r of tile t is row 32t + 16 (r / 8) + 8 half + r % 8.
+template <int DV, int KT, typename TS>
+__device__ __forceinline__ void load_state(f32x16 (&S)[KT], const TS* p, int lane, int col0) {
+  p += 8 * (lane >> 5) * DV + col0 + (lane & 31);
+#pragma unroll
+  for (int t = 0; t < KT; ++t)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) S[t][r] = (float)p[(32 * t + 16 * (r >> 3) + (r & 7)) * DV];
 }
-__device__ __forceinline__ void store_state1(void* p, int64_t i, float x, bool bf) {
-  if (bf) static_cast<bf16*>(p)[i] = (bf16)x;
-  else static_cast<float*>(p)[i] = x;
+template <int DV, int KT, typename TS>
+__device__ __forceinline__ void store_state(const f32x16 (&S)[KT], TS* p, int lane, int col0) {
+  p += 8 * (lane >> 5) * DV + col0 + (lane & 31);
+#pragma unroll
+  for (int t = 0; t < KT; ++t)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) p[(32 * t + 16 * (r >> 3) + (r & 7)) * DV] = (TS)S[t][r];
 }
 
 // A chunk's rows of one of q, k, v on their way from memory to LDS, as 16-byte
@@ -211,9 +222,7 @@ __global__ __launch_bounds__(2 * VW, sizeof(T) == 2 && VW == 128 && HG < 4 ? 2 :
   const bool sbf = P.state_bf16;
   const int64_t sbase = (slot * P.H + hb + hw) * (int64_t)(DK * DV);
   const int64_t wbase = ((s.slot + s.p) * P.H + hb + hw) * (int64_t)(DK * DV);
-  // lane's state element of tile t, register r: row 32t + 16 (r / 8) + 8 half + r % 8
-  const int lrow = 8 * half, lcol = 32 * w % DV + col;
-  auto at = [&](int t, int r) { return (32 * t + 16 * (r >> 3) + lrow + (r & 7)) * DV + lcol; };
+  const int col0 = 32 * w % DV;
 
   f32x16 S[KT];
 #pragma unroll
@@ -221,17 +230,9 @@ __global__ __launch_bounds__(2 * VW, sizeof(T) == 2 && VW == 128 && HG < 4 ? 2 :
 #pragma unroll
     for (int r = 0; r < 16; ++r) S[t][r] = 0.f;
   if (OUT) {
-    if (s.count > 1) {
-#pragma unroll
-      for (int t = 0; t < KT; ++t)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) S[t][r] = P.ws_state[wbase + at(t, r)];
-    } else if (P.h0) {
-#pragma unroll
-      for (int t = 0; t < KT; ++t)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) S[t][r] = load_state1(P.h0, sbase + at(t, r), sbf);
-    }
+    if (s.count > 1) load_state<DV>(S, P.ws_state + wbase, lane, col0);
+    else if (P.h0 && sbf) load_state<DV>(S, static_cast<const bf16*>(P.h0) + sbase, lane, col0);
+    else if (P.h0) load_state<DV>(S, static_cast<const float*>(P.h0) + sbase, lane, col0);
   }
 
   const int hk = hb / P.rep;
@@ -463,16 +464,11 @@ __global__ __launch_bounds__(2 * VW, sizeof(T) == 2 && VW == 128 && HG < 4 ? 2 :
 
   if (OUT) {
     if (P.ht && s.p + 1 >= s.count) {
-#pragma unroll
-      for (int t = 0; t < KT; ++t)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) store_state1(P.ht, sbase + at(t, r), S[t][r], sbf);
+      if (sbf) store_state<DV>(S, static_cast<bf16*>(P.ht) + sbase, lane, col0);
+      else store_state<DV>(S, static_cast<float*>(P.ht) + sbase, lane, col0);
     }
   } else {
-#pragma unroll
-    for (int t = 0; t < KT; ++t)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) P.ws_state[wbase + at(t, r)] = S[t][r];
+    store_state<DV>(S, P.ws_state + wbase, lane, col0);
     if (gwave && lane == 0) {
 #pragma unroll
       for (int x = 0; x < HG; ++x) P.ws_decay[(s.slot + s.p) * P.H + hb + x] = (float)logsum[x];
@@ -487,8 +483,17 @@ __global__ __launch_bounds__(256) void linear_join_kernel(LinearParams P, int el
   const int part = blockIdx.x % parts;
   const int nh = blockIdx.x / parts;
   const int h = nh % P.H;
-  const Segment s = sequence_of(P, nh / P.H);
-  if (s.count < 2) return;
+  // Workgroups go by the multiples of L inside the batch: a sequence of two or
+  // more segments holds one behind its first token, and its first such takes it.
+  const int64_t mark = (int64_t)(nh / P.H + 1) * P.L;
+  int lo = 0, hi = P.N - 1;
+  while (lo < hi) {  // the last n that starts before the mark
+    const int mid = (lo + hi + 1) >> 1;
+    if (cu_at(P, mid) < mark) lo = mid;
+    else hi = mid - 1;
+  }
+  const Segment s = sequence_of(P, lo);
+  if (s.count < 2 || s.begin / P.L + 1 != mark / P.L) return;
   const int64_t slot = slot_of(P, s.n);
   if (slot < 0) return;
   const int e = (part * 256 + threadIdx.x) * 4;
@@ -519,7 +524,7 @@ hipError_t launch(const LinearParams& p, bool split, hipStream_t stream) {
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const int parts = DK * DV / 1024;
-    linear_join_kernel<<<(unsigned)((int64_t)p.N * p.H * parts), 256, 0, stream>>>(p, DK * DV, parts);
+    linear_join_kernel<<<(unsigned)(p.T / p.L * p.H * parts), 256, 0, stream>>>(p, DK * DV, parts);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -555,11 +560,13 @@ int64_t ws_slots(int64_t T, int64_t L) { return 2 * (T / L) + 1; }
 }  // namespace
 
 int64_t linear_segment(int64_t t_total, int n_seqs, int n_heads) {
-  (void)n_seqs;
   // about two workgroups for each of the 256 CUs
   const int64_t want = (t_total * n_heads + 511) / 512;
   const int64_t seg = (want + C - 1) / C * C;
-  return seg < 256 ? 256 : seg;
+  // below that a split costs two launches more: taken for short sequences only
+  // when they alone leave CUs idle
+  const int64_t least = (int64_t)n_seqs * n_heads >= 256 ? 1024 : 256;
+  return seg < least ? least : seg;
 }
 
 size_t linear_workspace_bytes(const LinearPrefillArgs& a) {

@@ -61,7 +61,7 @@ def _prefill(al, over):
     (dict(n_k_heads=8), -2), (dict(dk=96), -4), (dict(dv=256), -4), (dict(decay=2), -4),
     (dict(t_total=-1), -2), (dict(t_total=1 << 31), -2), (dict(scale=float("nan")), -2),
     (dict(state_dtype=9), -3), (dict(dtype=1, state_dtype=2), -4),
-    (dict(n_seqs=40_000_000), -2),                                  # workgroups past 32 bits
+    (dict(n_seqs=600_000_000), -2),                                 # workgroups past 32 bits
     (dict(q_stride=64), -2), (dict(k_stride=132), -2), (dict(v_stride=1 << 29), -2),
     (dict(o_stride=-8), -2),
     (dict(state_indices=0x8000000, n_slots=0), -2),
