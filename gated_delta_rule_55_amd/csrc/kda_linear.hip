@@ -24,6 +24,8 @@
 // V' in bf16 would cost the carried state half its digits, so it is split into
 // three bf16 values (24 bits) and multiplied three times; q's copy of the
 // state and P are rounded to bf16 once, as o will be.
+#include <type_traits>
+
 #include "kda_linear_launch.h"
 #include "kda_linear_ops.h"
 
@@ -44,55 +46,128 @@ struct LinearParams {
   const int* slots;
   float* ws_state;  // [slot][H][dk][dv]
   float* ws_decay;  // [slot][H] natural log of a segment's decay
-  int64_t T, L;
+  int T, L;
+  unsigned int lmul, lshift;  // x / L = (x / 64) * lmul >> lshift
   int N, H, rep, n_slots;
   float scale;
   bool state_bf16, decay_head;
 };
 
-// Segment `id` of the launch.  Sequence n owns the ids from cu[n] / L + n on:
-// cu[n + 1] / L - cu[n] / L + 1 of them, at least its ceil(len / L) segments.
 struct Segment {
   int n, p, count;        // sequence, segment in it, its number of segments
-  int64_t begin, end;     // tokens
-  int64_t slot;           // workspace slot of segment 0
+  int begin, end;         // tokens
+  int slot;               // workspace slot of segment 0
 };
 
-__device__ __forceinline__ int64_t cu_at(const LinearParams& P, int n) {
+__device__ __forceinline__ int cu_at(const LinearParams& P, int n) {
   if (!P.cu) return n == 0 ? 0 : P.T;
-  const int64_t c = P.cu[n];
+  const int c = P.cu[n];
   return c < 0 ? 0 : c > P.T ? P.T : c;
 }
+__device__ __forceinline__ int div_l(const LinearParams& P, int x) {
+  return (int)(((uint64_t)((unsigned int)x >> 6) * P.lmul) >> P.lshift);
+}
 
-__device__ __forceinline__ Segment sequence_of(const LinearParams& P, int n) {
+// The segments of a sequence of `len` tokens: one (also of none), or equally
+// long ones but for the last; `each` is their length.
+__device__ __forceinline__ int count_segments(const LinearParams& P, int len, int& each) {
+  each = P.L;
+  if (len <= P.L) return 1;
+  const unsigned int most = div_l(P, len - 1) + 1;
+  each = (int)(((unsigned int)len + most - 1) / most + C - 1) / C * C;
+  return (int)(((unsigned int)len + each - 1) / (unsigned int)each);
+}
+
+__device__ __forceinline__ int len_at(const LinearParams& P, int n) {
+  const int len = cu_at(P, n + 1) - cu_at(P, n);
+  return len > 0 ? len : 0;
+}
+
+// Segment p of sequence n.
+__device__ __forceinline__ Segment segment_of(const LinearParams& P, int n, int p) {
   Segment s;
   s.n = n;
-  s.p = 0;
+  s.p = p;
   s.begin = cu_at(P, n);
-  const int64_t e = cu_at(P, n + 1);
-  s.end = e > s.begin ? e : s.begin;
-  s.count = (int)((s.end - s.begin + P.L - 1) / P.L);
+  const int len = len_at(P, n), end = s.begin + len;
   // sequences of two or more segments start in different L-token blocks, with
   // at least count - 1 blocks to the next such start: twice the block index
   // leaves room for count slots
-  s.slot = 2 * (s.begin / P.L);
+  s.slot = 2 * div_l(P, s.begin);
+  int each;
+  s.count = count_segments(P, len, each);
+  s.begin += p * each;
+  s.end = p + 1 < s.count ? s.begin + each : end;
   return s;
 }
 
+// Segment `id` of the launch, by one wave: all segments of all sequences
+// (LAST), or all but each sequence's last.  At most T / L + N exist.  Each lane
+// counts those of its run of sequences, a scan over the lanes finds the run.
+template <bool LAST>
 __device__ __forceinline__ bool find_segment(const LinearParams& P, int id, Segment& s) {
-  int lo = 0, hi = P.N - 1;
-  while (lo < hi) {  // the last n with cu[n] / L + n <= id
-    const int mid = (lo + hi + 1) >> 1;
-    if (cu_at(P, mid) / P.L + mid <= id) lo = mid;
-    else hi = mid - 1;
+  const int lane = threadIdx.x & 63;
+  const int per = (P.N + 63) / 64;
+  int mine = 0, each;
+  for (int i = 0; i < per; ++i) {
+    const int n = lane * per + i;
+    if (n < P.N) mine += count_segments(P, len_at(P, n), each) - !LAST;
   }
-  s = sequence_of(P, lo);
-  const int64_t p = id - (s.begin / P.L + lo);
-  if (p < 0 || p >= (s.count > 0 ? s.count : 1)) return false;
-  s.p = (int)p;
-  s.begin += p * P.L;
-  if (s.end > s.begin + P.L) s.end = s.begin + P.L;
+  int sum = mine;
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    const int x = __shfl_up(sum, off, 64);
+    if (lane >= off) sum += x;
+  }
+  const unsigned long long past = __ballot(sum > id);
+  if (past == 0) return false;
+  const int run = __builtin_ctzll(past);
+  int n = run * per, p = id - __builtin_amdgcn_readlane(sum - mine, run);
+  for (;;) {  // ends in the run: its segments are past id
+    const int here = count_segments(P, len_at(P, n), each) - !LAST;
+    if (p < here) break;
+    p -= here;
+    ++n;
+  }
+  s = segment_of(P, n, p);
   return true;
+}
+
+// The last n with key(n) <= x for a key that does not fall, by one wave: each
+// round narrows the range 64 times.
+template <typename Key>
+__device__ __forceinline__ int search(int n, int x, Key key) {
+  const int lane = threadIdx.x & 63;
+  int lo = 0;
+  while (n > 1) {
+    const int step = (n + 63) / 64;
+    const int at = lo + lane * step;
+    const bool in = lane * step < n && key(at) <= x;
+    const int hits = __popcll(__ballot(in));
+    const int skip = hits > 0 ? (hits - 1) * step : 0;
+    lo += skip;
+    n = n - skip < step ? n - skip : step;
+  }
+  return __builtin_amdgcn_readfirstlane(lo);
+}
+
+// Which segment id and head group a workgroup takes.  Workgroups go round the
+// 8 XCDs.  Where `share` groups of heads read one key head, these are 8 apart,
+// so that they read q and k through the same L2; without that, neighbours in
+// memory stay on different XCDs (the other way round cost 32,768 tokens x 32
+// heads a quarter).
+__device__ __forceinline__ void place(int groups, int share, int& id, int& group) {
+  int i = blockIdx.x;
+  if (share > 1) {
+    const int r = i / 8 % share;
+    i = (i / 8 / share * 8 + i % 8) * share + r;
+  }
+  id = i / groups;
+  group = i % groups;
+}
+inline int64_t placed_blocks(int64_t ids, int groups, int share) {
+  const int64_t n = ids * groups;
+  return share > 1 ? (n / share + 7) / 8 * 8 * share : n;
 }
 
 // The state slot of sequence n, or -1 to skip it.
@@ -209,10 +284,11 @@ __global__ __launch_bounds__(2 * VW, sizeof(T) == 2 && VW == 128 && HG < 4 ? 2 :
   __shared__ Smem<T, DK, VW, HG, OUT> sm;
 
   const int groups = P.H / HG;
-  const int hb = blockIdx.x % groups * HG;  // first head
+  int id, group;
+  place(groups, P.rep / HG, id, group);
+  const int hb = group * HG;  // first head
   Segment s;
-  if (!find_segment(P, blockIdx.x / groups, s)) return;
-  if (!OUT && s.p + 1 >= s.count) return;
+  if (!find_segment<OUT>(P, id, s)) return;
   const int64_t slot = slot_of(P, s.n);
   if (slot < 0) return;
 
@@ -221,7 +297,7 @@ __global__ __launch_bounds__(2 * VW, sizeof(T) == 2 && VW == 128 && HG < 4 ? 2 :
   const int hw = 32 * w / DV;  // this wave's head of the group
   const bool sbf = P.state_bf16;
   const int64_t sbase = (slot * P.H + hb + hw) * (int64_t)(DK * DV);
-  const int64_t wbase = ((s.slot + s.p) * P.H + hb + hw) * (int64_t)(DK * DV);
+  const int64_t wbase = ((int64_t)(s.slot + s.p) * P.H + hb + hw) * (int64_t)(DK * DV);
   const int col0 = 32 * w % DV;
 
   f32x16 S[KT];
@@ -242,7 +318,7 @@ __global__ __launch_bounds__(2 * VW, sizeof(T) == 2 && VW == 128 && HG < 4 ? 2 :
   const int qo = OUT ? RQ::offset(tid, P.qs) : 0, ko = RQ::offset(tid, P.ks), vo = RV::offset(tid, P.vs);
   RQ rq, rk;
   RV rv;
-  const int len = (int)(s.end - s.begin);
+  const int len = s.end - s.begin;
   auto valid_at = [&](int c0) { return len - c0 < C ? len - c0 : C; };
   auto fetch = [&](int c0) {
     const int valid = valid_at(c0);
@@ -265,7 +341,7 @@ __global__ __launch_bounds__(2 * VW, sizeof(T) == 2 && VW == 128 && HG < 4 ? 2 :
   auto fetch_g = [&](int c0) {
 #pragma unroll
     for (int x = 0; x < HG; ++x)
-      g[x] = P.decay_head ? P.g[hb + x] : lane < len - c0 ? P.g[(s.begin + c0 + lane) * P.H + hb + x] : 0.f;
+      g[x] = P.decay_head ? P.g[hb + x] : lane < len - c0 ? P.g[(int64_t)(s.begin + c0 + lane) * P.H + hb + x] : 0.f;
   };
   auto sum_g = [&](int c0, int b) {
 #pragma unroll
@@ -371,15 +447,16 @@ __global__ __launch_bounds__(2 * VW, sizeof(T) == 2 && VW == 128 && HG < 4 ? 2 :
 #pragma unroll
       for (int e = 0; e < 8; ++e) vd[e] = to_f32(vf[x][e]) * (e < 4 ? d0[e & 3] : d1[e & 3]);
       if constexpr (sizeof(T) == 2) {
-        bf16x8 va, vb2, vc;
-        split3(vd, va, vb2, vc);
+        bf16x8 vp[3];
+        split3(vd, vp[0], vp[1], vp[2]);
+        F kf[KT];
 #pragma unroll
-        for (int t = 0; t < KT; ++t) {
-          const F kf = frag_t<true>(sm.k + 16 * x * RQ::S + 32 * t, RQ::S, lane);
-          S[t] = mma(kf, vc, S[t]);
-          S[t] = mma(kf, vb2, S[t]);
-          S[t] = mma(kf, va, S[t]);
-        }
+        for (int t = 0; t < KT; ++t) kf[t] = frag_t<true>(sm.k + 16 * x * RQ::S + 32 * t, RQ::S, lane);
+        // the smallest part first; consecutive steps go to different tiles
+#pragma unroll
+        for (int part = 2; part >= 0; --part)
+#pragma unroll
+          for (int t = 0; t < KT; ++t) S[t] = mma(kf[t], vp[part], S[t]);
       } else {
 #pragma unroll
         for (int t = 0; t < KT; ++t)
@@ -432,7 +509,7 @@ __global__ __launch_bounds__(2 * VW, sizeof(T) == 2 && VW == 128 && HG < 4 ? 2 :
 #pragma unroll
       for (int it = 0; it < 2; ++it) {
         const int i = 32 * it + col;
-        T* op = static_cast<T*>(P.o) + (s.begin + c0 + i) * P.os + hb * DV + 32 * w;
+        T* op = static_cast<T*>(P.o) + (int64_t)(s.begin + c0 + i) * P.os + hb * DV + 32 * w;
         if constexpr (sizeof(T) == 2) {
           // the halves trade register groups, so that each holds 8 columns in a row
 #pragma unroll
@@ -471,60 +548,90 @@ __global__ __launch_bounds__(2 * VW, sizeof(T) == 2 && VW == 128 && HG < 4 ? 2 :
     store_state<DV>(S, P.ws_state + wbase, lane, col0);
     if (gwave && lane == 0) {
 #pragma unroll
-      for (int x = 0; x < HG; ++x) P.ws_decay[(s.slot + s.p) * P.H + hb + x] = (float)logsum[x];
+      for (int x = 0; x < HG; ++x) P.ws_decay[(int64_t)(s.slot + s.p) * P.H + hb + x] = (float)logsum[x];
     }
   }
 }
 
 // Pass 2: the state each segment of a split sequence starts from, in place of
-// the segments' own states.  A thread walks four elements through the
-// segments; 1 / (dk dv) of the arithmetic, bound by the workspace's traffic.
-__global__ __launch_bounds__(256) void linear_join_kernel(LinearParams P, int elems, int parts) {
-  const int part = blockIdx.x % parts;
+// the segments' own states.  A thread walks X vectors of four elements through
+// the segments, four segments loaded at a time; bound by the workspace's
+// traffic (32,768 tokens x 32 heads: 12 us), two vectors a thread keeping the
+// workgroups few, or by the walk where there are few of them: one vector then.
+// Workgroups go by sequence or, where there are more sequences than segment
+// lengths in the batch, by the multiples of L: a sequence of two or more
+// segments holds one behind its first token, and its first such takes it.
+template <int X>
+__global__ __launch_bounds__(256) void linear_join_kernel(LinearParams P, int elems, int parts, bool marks) {
+  const int e = (blockIdx.x % parts * 256 + threadIdx.x) * 4 * X;
   const int nh = blockIdx.x / parts;
   const int h = nh % P.H;
-  // Workgroups go by the multiples of L inside the batch: a sequence of two or
-  // more segments holds one behind its first token, and its first such takes it.
-  const int64_t mark = (int64_t)(nh / P.H + 1) * P.L;
-  int lo = 0, hi = P.N - 1;
-  while (lo < hi) {  // the last n that starts before the mark
-    const int mid = (lo + hi + 1) >> 1;
-    if (cu_at(P, mid) < mark) lo = mid;
-    else hi = mid - 1;
-  }
-  const Segment s = sequence_of(P, lo);
-  if (s.count < 2 || s.begin / P.L + 1 != mark / P.L) return;
+  int n = nh / P.H;
+  const int block = n + 1;
+  if (marks) n = search(P.N, block * P.L - 1, [&](int i) { return cu_at(P, i); });
+  const Segment s = segment_of(P, n, 0);
+  if (s.count < 2 || (marks && s.slot / 2 + 1 != block) || e >= elems) return;
   const int64_t slot = slot_of(P, s.n);
   if (slot < 0) return;
-  const int e = (part * 256 + threadIdx.x) * 4;
-  if (e >= elems) return;
-  f32x4 S = f32x4{0.f, 0.f, 0.f, 0.f};
+  f32x4 S[X];
+#pragma unroll
+  for (int x = 0; x < X; ++x) S[x] = zero4();
   if (P.h0) {
     const int64_t b = (slot * P.H + h) * (int64_t)elems + e;
-    S = P.state_bf16 ? load_state4(static_cast<const bf16*>(P.h0) + b)
-                     : load_state4(static_cast<const float*>(P.h0) + b);
+#pragma unroll
+    for (int x = 0; x < X; ++x)
+      S[x] = P.state_bf16 ? load_state4(static_cast<const bf16*>(P.h0) + b + 4 * x)
+                          : load_state4(static_cast<const float*>(P.h0) + b + 4 * x);
   }
   const int64_t step = (int64_t)P.H * elems;
-  float* p = P.ws_state + (s.slot * P.H + h) * (int64_t)elems + e;
-  const float* d = P.ws_decay + s.slot * P.H + h;
-  for (int i = 0; i < s.count; ++i, p += step, d += P.H) {
-    const bool last = i + 1 == s.count;
-    f32x4 own = last ? S : *reinterpret_cast<const f32x4*>(p);
-    *reinterpret_cast<f32x4*>(p) = S;
-    if (!last) S = S * fast_exp2(*d * kLog2e) + own;
-  }
+  float* p = P.ws_state + ((int64_t)s.slot * P.H + h) * elems + e;
+  const float* d = P.ws_decay + (int64_t)s.slot * P.H + h;
+  const int own = s.count - 1;  // segments with a state of their own
+  constexpr int B = 4;
+  auto walk = [&](auto count) {
+    constexpr int K = decltype(count)::value;
+    f32x4 own_s[K][X];
+    float dec[K];
+#pragma unroll
+    for (int j = 0; j < K; ++j) {
+#pragma unroll
+      for (int x = 0; x < X; ++x) own_s[j][x] = *reinterpret_cast<const f32x4*>(p + j * step + 4 * x);
+      dec[j] = d[j * P.H];
+    }
+#pragma unroll
+    for (int j = 0; j < K; ++j) {
+      const float f = fast_exp2(dec[j] * kLog2e);
+#pragma unroll
+      for (int x = 0; x < X; ++x) {
+        *reinterpret_cast<f32x4*>(p + j * step + 4 * x) = S[x];
+        S[x] = S[x] * f + own_s[j][x];
+      }
+    }
+    p += K * step;
+    d += K * P.H;
+  };
+  int i = 0;
+  for (; i + B <= own; i += B) walk(std::integral_constant<int, B>{});
+  for (; i < own; ++i) walk(std::integral_constant<int, 1>{});
+#pragma unroll
+  for (int x = 0; x < X; ++x) *reinterpret_cast<f32x4*>(p + 4 * x) = S[x];
 }
 
 template <typename T, int DK, int DV, int HG>
 hipError_t launch(const LinearParams& p, bool split, hipStream_t stream) {
-  const int64_t blocks = linear_segments(p.T, p.N, p.L) * (p.H / HG);
+  const int64_t blocks = placed_blocks(linear_segments(p.T, p.N, p.L), p.H / HG, p.rep / HG);
   constexpr int VW = DV * HG;
   if (split) {
     linear_kernel<T, DK, VW, HG, false><<<(unsigned)blocks, 2 * VW, 0, stream>>>(p);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    const int parts = DK * DV / 1024;
-    linear_join_kernel<<<(unsigned)(p.T / p.L * p.H * parts), 256, 0, stream>>>(p, DK * DV, parts);
+    constexpr int parts = DK * DV / 1024, parts2 = (parts + 1) / 2;
+    const bool marks = p.T / p.L < p.N;
+    const int64_t most = (int64_t)(marks ? p.T / p.L : p.N) * p.H;
+    if (most * parts <= 512)
+      linear_join_kernel<1><<<(unsigned)(most * parts), 256, 0, stream>>>(p, DK * DV, parts, marks);
+    else
+      linear_join_kernel<2><<<(unsigned)(most * parts2), 256, 0, stream>>>(p, DK * DV, parts2, marks);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -559,18 +666,22 @@ int64_t ws_slots(int64_t T, int64_t L) { return 2 * (T / L) + 1; }
 
 }  // namespace
 
-int64_t linear_segment(int64_t t_total, int n_seqs, int n_heads) {
-  // about two workgroups for each of the 256 CUs
-  const int64_t want = (t_total * n_heads + 511) / 512;
+int64_t linear_segment(int64_t t_total, int n_seqs, int n_heads, int dv) {
+  // about eight waves, of 32 value columns each, for each of the 256 CUs (one
+  // sequence of 32,768 tokens x 32 heads: 400 us, with twelve 455, sixteen 424);
+  // for several sequences, whose segments are not equally long, twelve (eight of
+  // 33,001 tokens in all: 395 us, with eight or sixteen 455 to 460)
+  const int64_t waves = n_seqs == 1 ? 2048 : 3072;
+  const int64_t want = (t_total * n_heads * (dv / 32) + waves - 1) / waves;
   const int64_t seg = (want + C - 1) / C * C;
   // below that a split costs two launches more: taken for short sequences only
   // when they alone leave CUs idle
-  const int64_t least = (int64_t)n_seqs * n_heads >= 256 ? 1024 : 256;
+  const int64_t least = (int64_t)n_seqs * n_heads >= 256 ? 1024 : 128;
   return seg < least ? least : seg;
 }
 
 size_t linear_workspace_bytes(const LinearPrefillArgs& a) {
-  const int64_t L = linear_segment(a.t_total, a.n_seqs, a.n_heads);
+  const int64_t L = linear_segment(a.t_total, a.n_seqs, a.n_heads, a.dv);
   if (a.t_total <= L) return 0;
   const int64_t slots = ws_slots(a.t_total, L);
   return decay_bytes(slots, a.n_heads) + (size_t)slots * a.n_heads * a.dk * a.dv * 4;
@@ -591,8 +702,14 @@ hipError_t launch_linear_prefill(const LinearPrefillArgs& a, void* workspace, hi
   p.ht = a.ht;
   p.cu = a.cu_seqlens;
   p.slots = a.slots;
-  p.T = a.t_total;
-  p.L = linear_segment(a.t_total, a.n_seqs, a.n_heads);
+  p.T = (int)a.t_total;
+  p.L = (int)linear_segment(a.t_total, a.n_seqs, a.n_heads, a.dv);
+  // x / 64 < 2^25 and L / 64 <= 2^k: exact with lmul = ceil(2^(25 + k) / (L / 64))
+  const uint64_t l = (uint64_t)p.L / 64;
+  unsigned int k = 0;
+  while (((uint64_t)1 << k) < l) ++k;
+  p.lshift = 25 + k;
+  p.lmul = (unsigned int)((((uint64_t)1 << p.lshift) + l - 1) / l);
   p.N = a.n_seqs;
   p.H = a.n_heads;
   p.rep = a.n_heads / a.kheads;

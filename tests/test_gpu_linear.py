@@ -367,3 +367,22 @@ def test_offsets_past_32_bits(kda):
     pool[slots.long()] = d["h0"]
     op, _ = kda.linear_prefill(d["q"], d["k"], d["v"], d["g"], pool, d["cu"], state_indices=slots)
     check_linear(i, op, pool[slots.long()])
+
+
+@pytest.mark.parametrize("n", [64, 65, 200, 1000])
+def test_prefill_many_sequences(kda, n):
+    """More sequences than lanes, empty and long ones among them."""
+    rng = np.random.default_rng(n)
+    lengths = rng.integers(0, 9, size=n)
+    lengths[rng.integers(0, n, size=2)] = (700, 1500)
+    i = linear_inputs(23, [int(x) for x in lengths], 2, 2, 32, 32, BF, g_scale=0.1)
+    o, ht = run(kda, cuda(i))
+    check_linear(i, o, ht)
+
+
+@pytest.mark.parametrize("H,Hk,dk,dv", [(8, 2, 64, 32), (8, 4, 32, 64), (12, 1, 64, 64), (6, 6, 128, 128), (4, 1, 128, 32)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_prefill_heads_sharing_a_key_head(kda, H, Hk, dk, dv, dtype):
+    i = linear_inputs(24, [500, 3, 0, 90], H, Hk, dk, dv, dtype, g_scale=0.2)
+    o, ht = run(kda, cuda(i))
+    check_linear(i, o, ht)
