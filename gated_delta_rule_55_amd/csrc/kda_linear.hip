@@ -57,7 +57,14 @@ struct Segment {
   int n, p, count;        // sequence, segment in it, its number of segments
   int begin, end;         // tokens
   int slot;               // workspace slot of segment 0
+  int state;              // state slot of the sequence, negative: skip it
 };
+
+__device__ __forceinline__ int state_at(const LinearParams& P, int n) {
+  if (!P.slots) return n;
+  const int s = P.slots[n];
+  return s < P.n_slots ? s : -1;
+}
 
 __device__ __forceinline__ int cu_at(const LinearParams& P, int n) {
   if (!P.cu) return n == 0 ? 0 : P.T;
@@ -78,26 +85,22 @@ __device__ __forceinline__ int count_segments(const LinearParams& P, int len, in
   return (int)(((unsigned int)len + each - 1) / (unsigned int)each);
 }
 
-__device__ __forceinline__ int len_at(const LinearParams& P, int n) {
-  const int len = cu_at(P, n + 1) - cu_at(P, n);
-  return len > 0 ? len : 0;
-}
+__device__ __forceinline__ int len_of(int begin, int end) { return end > begin ? end - begin : 0; }
 
-// Segment p of sequence n.
-__device__ __forceinline__ Segment segment_of(const LinearParams& P, int n, int p) {
+// Segment p of sequence n, which has `len` tokens from `begin`.
+__device__ __forceinline__ Segment segment_of(const LinearParams& P, int n, int p, int begin, int len, int state) {
   Segment s;
   s.n = n;
   s.p = p;
-  s.begin = cu_at(P, n);
-  const int len = len_at(P, n), end = s.begin + len;
+  s.state = state;
   // sequences of two or more segments start in different L-token blocks, with
   // at least count - 1 blocks to the next such start: twice the block index
   // leaves room for count slots
-  s.slot = 2 * div_l(P, s.begin);
+  s.slot = 2 * div_l(P, begin);
   int each;
   s.count = count_segments(P, len, each);
-  s.begin += p * each;
-  s.end = p + 1 < s.count ? s.begin + each : end;
+  s.begin = begin + p * each;
+  s.end = p + 1 < s.count ? s.begin + each : begin + len;
   return s;
 }
 
@@ -108,10 +111,15 @@ template <bool LAST>
 __device__ __forceinline__ bool find_segment(const LinearParams& P, int id, Segment& s) {
   const int lane = threadIdx.x & 63;
   const int per = (P.N + 63) / 64;
-  int mine = 0, each;
+  int mine = 0, each, begin = 0, len = 0, state = -1;
   for (int i = 0; i < per; ++i) {
     const int n = lane * per + i;
-    if (n < P.N) mine += count_segments(P, len_at(P, n), each) - !LAST;
+    if (n < P.N) {
+      begin = cu_at(P, n);
+      len = len_of(begin, cu_at(P, n + 1));
+      if (per == 1) state = state_at(P, n);
+      mine += count_segments(P, len, each) - !LAST;
+    }
   }
   int sum = mine;
 #pragma unroll
@@ -123,13 +131,19 @@ __device__ __forceinline__ bool find_segment(const LinearParams& P, int id, Segm
   if (past == 0) return false;
   const int run = __builtin_ctzll(past);
   int n = run * per, p = id - __builtin_amdgcn_readlane(sum - mine, run);
-  for (;;) {  // ends in the run: its segments are past id
-    const int here = count_segments(P, len_at(P, n), each) - !LAST;
+  if (per == 1) {
+    s = segment_of(P, n, p, __builtin_amdgcn_readlane(begin, run), __builtin_amdgcn_readlane(len, run),
+                   __builtin_amdgcn_readlane(state, run));
+    return true;
+  }
+  for (;; ++n) {  // ends in the run: its segments are past id
+    begin = cu_at(P, n);
+    len = len_of(begin, cu_at(P, n + 1));
+    const int here = count_segments(P, len, each) - !LAST;
     if (p < here) break;
     p -= here;
-    ++n;
   }
-  s = segment_of(P, n, p);
+  s = segment_of(P, n, p, begin, len, state_at(P, n));
   return true;
 }
 
@@ -168,13 +182,6 @@ __device__ __forceinline__ void place(int groups, int share, int& id, int& group
 inline int64_t placed_blocks(int64_t ids, int groups, int share) {
   const int64_t n = ids * groups;
   return share > 1 ? (n / share + 7) / 8 * 8 * share : n;
-}
-
-// The state slot of sequence n, or -1 to skip it.
-__device__ __forceinline__ int64_t slot_of(const LinearParams& P, int n) {
-  if (!P.slots) return n;
-  const int s = P.slots[n];
-  return s >= 0 && s < P.n_slots ? s : -1;
 }
 
 // A wave's part of a state in memory, [DK][DV] at p of type TS, to or from its
@@ -289,27 +296,15 @@ __global__ __launch_bounds__(2 * VW, sizeof(T) == 2 && VW == 128 && HG < 4 ? 2 :
   const int hb = group * HG;  // first head
   Segment s;
   if (!find_segment<OUT>(P, id, s)) return;
-  const int64_t slot = slot_of(P, s.n);
-  if (slot < 0) return;
+  if (s.state < 0) return;
 
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
   const int half = lane >> 5, col = lane & 31;
   const int hw = 32 * w / DV;  // this wave's head of the group
   const bool sbf = P.state_bf16;
-  const int64_t sbase = (slot * P.H + hb + hw) * (int64_t)(DK * DV);
-  const int64_t wbase = ((int64_t)(s.slot + s.p) * P.H + hb + hw) * (int64_t)(DK * DV);
+  const int64_t sbase = ((int64_t)s.state * P.H + hb + hw) * (DK * DV);
+  const int64_t wbase = ((int64_t)(s.slot + s.p) * P.H + hb + hw) * (DK * DV);
   const int col0 = 32 * w % DV;
-
-  f32x16 S[KT];
-#pragma unroll
-  for (int t = 0; t < KT; ++t)
-#pragma unroll
-    for (int r = 0; r < 16; ++r) S[t][r] = 0.f;
-  if (OUT) {
-    if (s.count > 1) load_state<DV>(S, P.ws_state + wbase, lane, col0);
-    else if (P.h0 && sbf) load_state<DV>(S, static_cast<const bf16*>(P.h0) + sbase, lane, col0);
-    else if (P.h0) load_state<DV>(S, static_cast<const float*>(P.h0) + sbase, lane, col0);
-  }
 
   const int hk = hb / P.rep;
   const T* qb = OUT ? static_cast<const T*>(P.q) + s.begin * P.qs + hk * DK : nullptr;
@@ -348,10 +343,23 @@ __global__ __launch_bounds__(2 * VW, sizeof(T) == 2 && VW == 128 && HG < 4 ? 2 :
     for (int x = 0; x < HG; ++x) logsum[x] += decay_sums(sm.d[b][x], g[x], P.decay_head, valid_at(c0), lane);
   };
 
+  // what is needed first is asked for first
   if (len > 0) {
+    if (gwave) fetch_g(0);
     fetch(0);
+  }
+  f32x16 S[KT];
+#pragma unroll
+  for (int t = 0; t < KT; ++t)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) S[t][r] = 0.f;
+  if (OUT) {
+    if (s.count > 1) load_state<DV>(S, P.ws_state + wbase, lane, col0);
+    else if (P.h0 && sbf) load_state<DV>(S, static_cast<const bf16*>(P.h0) + sbase, lane, col0);
+    else if (P.h0) load_state<DV>(S, static_cast<const float*>(P.h0) + sbase, lane, col0);
+  }
+  if (len > 0) {
     if (gwave) {
-      fetch_g(0);
       sum_g(0, 0);
       fetch_g(C);
     }
@@ -569,15 +577,14 @@ __global__ __launch_bounds__(256) void linear_join_kernel(LinearParams P, int el
   int n = nh / P.H;
   const int block = n + 1;
   if (marks) n = search(P.N, block * P.L - 1, [&](int i) { return cu_at(P, i); });
-  const Segment s = segment_of(P, n, 0);
-  if (s.count < 2 || (marks && s.slot / 2 + 1 != block) || e >= elems) return;
-  const int64_t slot = slot_of(P, s.n);
-  if (slot < 0) return;
+  const int begin = cu_at(P, n);
+  const Segment s = segment_of(P, n, 0, begin, len_of(begin, cu_at(P, n + 1)), state_at(P, n));
+  if (s.count < 2 || (marks && s.slot / 2 + 1 != block) || e >= elems || s.state < 0) return;
   f32x4 S[X];
 #pragma unroll
   for (int x = 0; x < X; ++x) S[x] = zero4();
   if (P.h0) {
-    const int64_t b = (slot * P.H + h) * (int64_t)elems + e;
+    const int64_t b = ((int64_t)s.state * P.H + h) * elems + e;
 #pragma unroll
     for (int x = 0; x < X; ++x)
       S[x] = P.state_bf16 ? load_state4(static_cast<const bf16*>(P.h0) + b + 4 * x)
