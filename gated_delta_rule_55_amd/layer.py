@@ -29,21 +29,14 @@ def _guard(dev, stream):
                 yield
 
 
-class _Here:
-    def __enter__(self):
-        pass
-
-    def __exit__(self, *exc):
-        pass
-
-
-_HERE = _Here()
+_HERE = contextlib.nullcontext()
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _on(dev, stream):
     """A context in which `dev` is current and `stream` (or the device's current
     stream) is the stream that torch allocates for."""
-    if stream is None and dev.index == torch.cuda.current_device():
+    if stream is None and dev.index == _current_device():
         return _HERE
     return _guard(dev, stream)
 
@@ -98,7 +91,7 @@ def _linear_common(what, q, v):
     if not (isinstance(q, torch.Tensor) and isinstance(v, torch.Tensor)):
         raise TypeError(f"{what}: q and v must be tensors")
     dev, dtype = q.device, q.dtype
-    if dev.type != "cuda":
+    if not q.is_cuda:
         raise ValueError(f"{what} runs on the GPU only")
     if dtype not in _DTYPES:
         raise TypeError(f"unsupported dtype {dtype}")
@@ -239,11 +232,11 @@ def linear_decode(state: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torc
             op, os_ = out.data_ptr(), 0
         else:
             op, os_ = _rows3(out, "out", (N, H, dv), dt, dev)
-        desc = _al.LinearDecodeDesc(
-            ctypes.sizeof(_al.LinearDecodeDesc), _DTYPES[dt], N, H, Hk, dk, dv, decay,
+        desc = _al.LINEAR_DECODE.pack(
+            _al.LINEAR_DECODE.size, _DTYPES[dt], N, H, Hk, dk, dv, decay,
             0.0 if scale is None else scale, _DTYPES[state.dtype], sp, qp, kp, vp, gp, op,
-            qs, ks, vs, os_, idxp, S if idxp is not None else 0)
-        st = _al.lib().kda_linear_decode(ctypes.byref(desc), _raw_stream(dev))
+            qs, ks, vs, os_, idxp or 0, S if idxp is not None else 0)
+        st = _al.lib().kda_linear_decode(desc, _raw_stream(dev))
     if st != _abi.KDA_OK:
         raise _abi.KdaError(st, "kda_linear_decode")
     return out
@@ -256,7 +249,7 @@ _GATES = {None: _al.KDA_NORM_GATE_LINEAR, "none": _al.KDA_NORM_GATE_LINEAR,
 def _norm_common(what, x, activation):
     if not isinstance(x, torch.Tensor) or x.dim() < 1:
         raise TypeError("x must be a tensor [..., dim]")
-    if x.device.type != "cuda":
+    if not x.is_cuda:
         raise ValueError(f"{what} runs on the GPU only")
     if x.dtype not in _DTYPES:
         raise TypeError(f"unsupported dtype {x.dtype}")
@@ -288,8 +281,8 @@ def _rows(t, name, shape, dtype, dev) -> Tuple[int, int]:
     return t.data_ptr(), row
 
 
-def _weight(w, name, dim, dev) -> Optional[int]:
-    return None if w is None else _dense(w, name, (dim,), torch.float32, dev)
+def _weight(w, name, dim, dev) -> int:
+    return 0 if w is None else _dense(w, name, (dim,), torch.float32, dev)
 
 
 def gated_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
@@ -307,7 +300,7 @@ def gated_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
     shape = x.shape
     xp, xs = _rows(x, "x", shape, dt, dev)
     wp = _weight(weight, "weight", dim, dev)
-    zp, zs = (None, 0) if gate is None else _rows(gate, "gate", shape, dt, dev)
+    zp, zs = (0, 0) if gate is None else _rows(gate, "gate", shape, dt, dev)
     with _on(dev, stream):
         if out is None:
             out = x.new_empty(shape)
@@ -316,10 +309,10 @@ def gated_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
             yp, ys = _rows(out, "out", shape, dt, dev)
         if dim == 0:
             return out
-        desc = _al.GatedNormDesc(
-            ctypes.sizeof(_al.GatedNormDesc), _DTYPES[dt], dim, _GATES[activation],
-            1 if gate_first else 0, eps, x.numel() // dim, xp, wp, zp, yp, xs, zs, ys)
-        st = _al.lib().kda_gated_norm(ctypes.byref(desc), _raw_stream(dev))
+        desc = _al.GATED_NORM.pack(
+            _al.GATED_NORM.size, _DTYPES[dt], dim, _GATES[activation], 1 if gate_first else 0, eps,
+            x.numel() // dim, xp, wp, zp, yp, xs, zs, ys)
+        st = _al.lib().kda_gated_norm(desc, _raw_stream(dev))
     if st != _abi.KDA_OK:
         raise _abi.KdaError(st, "kda_gated_norm")
     return out
@@ -354,7 +347,7 @@ def block_norm(x: torch.Tensor, residual: torch.Tensor,
     wpost = _weight(weight_post, "weight_post", dim, dev)
     wpre = _weight(weight_pre, "weight_pre", dim, dev)
     cp = _weight(channel_scale, "channel_scale", dim, dev)
-    zp, zs = (None, 0) if gate is None else _rows(gate, "gate", shape, dt, dev)
+    zp, zs = (0, 0) if gate is None else _rows(gate, "gate", shape, dt, dev)
     if out is not None and weight_pre is None:
         raise ValueError("out needs weight_pre")
     with _on(dev, stream):
@@ -363,7 +356,7 @@ def block_norm(x: torch.Tensor, residual: torch.Tensor,
             rop, ros = residual_out.data_ptr(), 0
         else:
             rop, ros = _rows(residual_out, "residual_out", shape, rd, dev)
-        yp, ys = None, 0
+        yp, ys = 0, 0
         if weight_pre is not None:
             if out is None:
                 out = x.new_empty(shape)
@@ -372,10 +365,10 @@ def block_norm(x: torch.Tensor, residual: torch.Tensor,
                 yp, ys = _rows(out, "out", shape, dt, dev)
         if dim == 0:
             return residual_out, out
-        desc = _al.BlockNormDesc(
-            ctypes.sizeof(_al.BlockNormDesc), _DTYPES[dt], _DTYPES[rd], dim, _GATES[activation],
-            eps, scale, x.numel() // dim, xp, rp, wpost, wpre, cp, zp, rop, yp, xs, rs, zs, ros, ys)
-        st = _al.lib().kda_block_norm(ctypes.byref(desc), _raw_stream(dev))
+        desc = _al.BLOCK_NORM.pack(
+            _al.BLOCK_NORM.size, _DTYPES[dt], _DTYPES[rd], dim, _GATES[activation], eps, scale,
+            x.numel() // dim, xp, rp, wpost, wpre, cp, zp, rop, yp, xs, rs, zs, ros, ys)
+        st = _al.lib().kda_block_norm(desc, _raw_stream(dev))
     if st != _abi.KDA_OK:
         raise _abi.KdaError(st, "kda_block_norm")
     return residual_out, out

@@ -211,3 +211,13 @@ def test_row_strides_of_views():
         layer._rows3(torch.zeros(5, 32, 2).transpose(1, 2), "q", (5, 2, 32), torch.float32, dev)
     with pytest.raises(ValueError):
         layer._rows3(torch.zeros(1, 1, 32).expand(5, 2, 32), "q", (5, 2, 32), torch.float32, dev)
+
+
+def test_packed_descriptors_match_the_structures(al):
+    """struct.pack and the ctypes structures lay out the same bytes."""
+    vals = dict(al.LinearDecodeDesc._fields_)
+    for fmt, cls in ((al.LINEAR_DECODE, al.LinearDecodeDesc), (al.GATED_NORM, al.GatedNormDesc),
+                     (al.BLOCK_NORM, al.BlockNormDesc)):
+        args = [i + 0.5 if t is ctypes.c_float else i + 3 for i, (_, t) in enumerate(cls._fields_)]
+        assert fmt.pack(*args) == bytes(cls(*args))
+    assert vals["n_slots"] is ctypes.c_int32
