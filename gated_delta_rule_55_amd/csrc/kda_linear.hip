@@ -104,49 +104,6 @@ __device__ __forceinline__ Segment segment_of(const LinearParams& P, int n, int 
   return s;
 }
 
-// Segment `id` of the launch, by one wave: all segments of all sequences
-// (LAST), or all but each sequence's last.  At most T / L + N exist.  Each lane
-// counts those of its run of sequences, a scan over the lanes finds the run.
-template <bool LAST>
-__device__ __forceinline__ bool find_segment(const LinearParams& P, int id, Segment& s) {
-  const int lane = threadIdx.x & 63;
-  const int per = (P.N + 63) / 64;
-  int mine = 0, each, begin = 0, len = 0, state = -1;
-  for (int i = 0; i < per; ++i) {
-    const int n = lane * per + i;
-    if (n < P.N) {
-      begin = cu_at(P, n);
-      len = len_of(begin, cu_at(P, n + 1));
-      if (per == 1) state = state_at(P, n);
-      mine += count_segments(P, len, each) - !LAST;
-    }
-  }
-  int sum = mine;
-#pragma unroll
-  for (int off = 1; off < 64; off <<= 1) {
-    const int x = __shfl_up(sum, off, 64);
-    if (lane >= off) sum += x;
-  }
-  const unsigned long long past = __ballot(sum > id);
-  if (past == 0) return false;
-  const int run = __builtin_ctzll(past);
-  int n = run * per, p = id - __builtin_amdgcn_readlane(sum - mine, run);
-  if (per == 1) {
-    s = segment_of(P, n, p, __builtin_amdgcn_readlane(begin, run), __builtin_amdgcn_readlane(len, run),
-                   __builtin_amdgcn_readlane(state, run));
-    return true;
-  }
-  for (;; ++n) {  // ends in the run: its segments are past id
-    begin = cu_at(P, n);
-    len = len_of(begin, cu_at(P, n + 1));
-    const int here = count_segments(P, len, each) - !LAST;
-    if (p < here) break;
-    p -= here;
-  }
-  s = segment_of(P, n, p, begin, len, state_at(P, n));
-  return true;
-}
-
 // The last n with key(n) <= x for a key that does not fall, by one wave: each
 // round narrows the range 64 times.
 template <typename Key>
@@ -163,6 +120,49 @@ __device__ __forceinline__ int search(int n, int x, Key key) {
     n = n - skip < step ? n - skip : step;
   }
   return __builtin_amdgcn_readfirstlane(lo);
+}
+
+// Segment `id` of the launch, by one wave: of all segments of all sequences
+// (LAST), or of all but each sequence's last; at most T / L + N exist, and
+// false comes back for ids without one.  Up to 64 sequences are counted by a
+// lane each, and a scan numbers their segments without gaps.  Beyond that
+// sequence n owns the T / L + N numbers from cu[n] / L + n on:
+// cu[n + 1] / L - cu[n] / L + 1 of them, at least its ceil(len / L); those that
+// it does not need are left out (counting 2,048 sequences of 32 tokens in every
+// workgroup took 4.9 ms for what this does in 1.5).
+template <bool LAST>
+__device__ __forceinline__ bool find_segment(const LinearParams& P, int id, Segment& s) {
+  if (P.N <= 64) {
+    const int lane = threadIdx.x & 63;
+    int mine = 0, each, begin = 0, len = 0, state = -1;
+    if (lane < P.N) {
+      begin = cu_at(P, lane);
+      len = len_of(begin, cu_at(P, lane + 1));
+      state = state_at(P, lane);
+      mine = count_segments(P, len, each) - !LAST;
+    }
+    int sum = mine;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const int x = __shfl_up(sum, off, 64);
+      if (lane >= off) sum += x;
+    }
+    const unsigned long long past = __ballot(sum > id);
+    if (past == 0) return false;
+    const int n = __builtin_ctzll(past);
+    s = segment_of(P, n, id - __builtin_amdgcn_readlane(sum - mine, n), __builtin_amdgcn_readlane(begin, n),
+                   __builtin_amdgcn_readlane(len, n), __builtin_amdgcn_readlane(state, n));
+    return true;
+  }
+  // even numbers first: sequences of just L tokens leave out every other one,
+  // which would leave every other XCD without work
+  const int ids = div_l(P, P.T) + P.N, evens = (ids + 1) / 2;
+  id = id < evens ? 2 * id : 2 * (id - evens) + 1;
+  const int n = search(P.N, id, [&](int i) { return div_l(P, cu_at(P, i)) + i; });
+  const int begin = cu_at(P, n);
+  const int p = id - (div_l(P, begin) + n);
+  s = segment_of(P, n, p, begin, len_of(begin, cu_at(P, n + 1)), state_at(P, n));
+  return p >= 0 && p < s.count - !LAST;
 }
 
 // Which segment id and head group a workgroup takes.  Workgroups go round the
@@ -673,7 +673,7 @@ int64_t ws_slots(int64_t T, int64_t L) { return 2 * (T / L) + 1; }
 
 }  // namespace
 
-int64_t linear_segment(int64_t t_total, int n_seqs, int n_heads, int dv) {
+int64_t linear_segment(int64_t t_total, int n_seqs, int n_heads, int dv, bool bf16) {
   // about eight waves, of 32 value columns each, for each of the 256 CUs (one
   // sequence of 32,768 tokens x 32 heads: 400 us, with twelve 455, sixteen 424);
   // for several sequences, whose segments are not equally long, twelve (eight of
@@ -682,13 +682,15 @@ int64_t linear_segment(int64_t t_total, int n_seqs, int n_heads, int dv) {
   const int64_t want = (t_total * n_heads * (dv / 32) + waves - 1) / waves;
   const int64_t seg = (want + C - 1) / C * C;
   // below that a split costs two launches more: taken for short sequences only
-  // when they alone leave CUs idle
-  const int64_t least = (int64_t)n_seqs * n_heads >= 256 ? 1024 : 128;
+  // when they alone leave CUs idle (512 tokens x 32 heads in bf16: 31 us against
+  // 32 in one segment, 1,024: 36 against 59), and not for 256 tokens (26 against
+  // 19; in fp32, whose chunks take twice as long, 36 against 42)
+  const int64_t least = (int64_t)n_seqs * n_heads >= 256 ? 1024 : bf16 && t_total <= 256 ? 256 : 128;
   return seg < least ? least : seg;
 }
 
 size_t linear_workspace_bytes(const LinearPrefillArgs& a) {
-  const int64_t L = linear_segment(a.t_total, a.n_seqs, a.n_heads, a.dv);
+  const int64_t L = linear_segment(a.t_total, a.n_seqs, a.n_heads, a.dv, a.bf16);
   if (a.t_total <= L) return 0;
   const int64_t slots = ws_slots(a.t_total, L);
   return decay_bytes(slots, a.n_heads) + (size_t)slots * a.n_heads * a.dk * a.dv * 4;
@@ -710,7 +712,7 @@ hipError_t launch_linear_prefill(const LinearPrefillArgs& a, void* workspace, hi
   p.cu = a.cu_seqlens;
   p.slots = a.slots;
   p.T = (int)a.t_total;
-  p.L = (int)linear_segment(a.t_total, a.n_seqs, a.n_heads, a.dv);
+  p.L = (int)linear_segment(a.t_total, a.n_seqs, a.n_heads, a.dv, a.bf16);
   // x / 64 < 2^25 and L / 64 <= 2^k: exact with lmul = ceil(2^(25 + k) / (L / 64))
   const uint64_t l = (uint64_t)p.L / 64;
   unsigned int k = 0;

@@ -70,7 +70,7 @@ int check_linear(const kda_linear_prefill_desc* d, kda::LinearPrefillArgs* a) {
   a->t_total = d->t_total;
   a->scale = d->scale != 0.f ? d->scale : 1.0f / std::sqrt((float)d->dk);
   // workgroups: segments x heads, and 8 per segment length and head that join them
-  const int64_t seg = kda::linear_segment(a->t_total, a->n_seqs, a->n_heads, a->dv);
+  const int64_t seg = kda::linear_segment(a->t_total, a->n_seqs, a->n_heads, a->dv, a->bf16);
   if ((kda::linear_segments(a->t_total, a->n_seqs, seg) + 8) * H > INT32_MAX ||
       a->t_total / seg * H * 8 > INT32_MAX)
     return KDA_ERR_SHAPE;

@@ -43,7 +43,7 @@ struct LinearDecodeArgs {
 };
 
 // Tokens per segment: a sequence longer than this is split (kda_linear.hip).
-int64_t linear_segment(int64_t t_total, int n_seqs, int n_heads, int dv);
+int64_t linear_segment(int64_t t_total, int n_seqs, int n_heads, int dv, bool bf16);
 // Workgroups per head of a segmented launch: at most t_total / seg + n_seqs
 // segments exist.
 inline int64_t linear_segments(int64_t t_total, int n_seqs, int64_t seg) {
