@@ -8,7 +8,7 @@
 // lanes and, for rows wider than a wave, through LDS.  A workgroup walks
 // several rows and keeps its columns' weights in registers.  Vectors need
 // only their elements' alignment (the hardware takes unaligned 16-byte
-// accesses); the columns of an incomplete last vector are moved one by one.
+// accesses).
 #include "kda_device.h"
 #include "kda_norm_launch.h"
 
@@ -23,39 +23,82 @@ struct Vec {
   typedef T type __attribute__((ext_vector_type(N), aligned(sizeof(T))));
 };
 
-// N columns of a row from column c on, as fp32; columns past dim as 0.
-template <typename T, int N>
-__device__ __forceinline__ void load_cols(const T* row, int c, int dim, float (&f)[N]) {
-  constexpr int VN = Vec<T>::N;
-  if (c + N <= dim) {
+// A thread's columns of a row: NI vectors of N, the i-th being vector
+// i TPR + lane of the row's whole vectors, and one column of the row's rest
+// (fewer than N columns, one each for the first lanes; N <= TPR).  What lies
+// past the row's end is 0 and is not stored.
+template <int NI, int N>
+struct Columns {
+  float v[NI][N];
+  float rest;
+
+  template <typename F>
+  __device__ __forceinline__ void each(F f) {
 #pragma unroll
-    for (int b = 0; b < N; b += VN) {
-      const typename Vec<T>::type v = *reinterpret_cast<const typename Vec<T>::type*>(row + c + b);
+    for (int i = 0; i < NI; ++i)
 #pragma unroll
-      for (int e = 0; e < VN; ++e) f[b + e] = to_f32((T)v[e]);
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < N; ++e) f[e] = c + e < dim ? to_f32(row[c + e]) : 0.f;
+      for (int e = 0; e < N; ++e) f(v[i][e]);
+    f(rest);
   }
-}
-template <typename T, int N>
-__device__ __forceinline__ void store_cols(T* row, int c, int dim, const float (&f)[N]) {
-  constexpr int VN = Vec<T>::N;
-  if (c + N <= dim) {
+  // f(this value, o's value of the same column)
+  template <typename F>
+  __device__ __forceinline__ void with(const Columns& o, F f) {
 #pragma unroll
-    for (int b = 0; b < N; b += VN) {
-      typename Vec<T>::type v;
+    for (int i = 0; i < NI; ++i)
 #pragma unroll
-      for (int e = 0; e < VN; ++e) v[e] = from_f32<T>(f[b + e]);
-      *reinterpret_cast<typename Vec<T>::type*>(row + c + b) = v;
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < N; ++e)
-      if (c + e < dim) row[c + e] = from_f32<T>(f[e]);
+      for (int e = 0; e < N; ++e) f(v[i][e], o.v[i][e]);
+    f(rest, o.rest);
   }
-}
+  __device__ __forceinline__ void fill(float x) {
+    each([&](float& y) { y = x; });
+  }
+  __device__ __forceinline__ float squares() {
+    float s = 0.f;
+    each([&](float& x) { s += x * x; });
+    return s;
+  }
+
+  template <int TPR, typename T>
+  __device__ __forceinline__ void load(const T* row, int lane, int dim) {
+    constexpr int VN = Vec<T>::N;
+    const int whole = dim / N;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const int c = i * TPR + lane;
+#pragma unroll
+      for (int e = 0; e < N; ++e) v[i][e] = 0.f;
+      if (c < whole) {
+#pragma unroll
+        for (int b = 0; b < N; b += VN) {
+          const typename Vec<T>::type x = *reinterpret_cast<const typename Vec<T>::type*>(row + c * N + b);
+#pragma unroll
+          for (int e = 0; e < VN; ++e) v[i][b + e] = to_f32((T)x[e]);
+        }
+      }
+    }
+    rest = 0.f;
+    if (whole * N + lane < dim) rest = to_f32(row[whole * N + lane]);
+  }
+  template <int TPR, typename T>
+  __device__ __forceinline__ void store(T* row, int lane, int dim) const {
+    constexpr int VN = Vec<T>::N;
+    const int whole = dim / N;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const int c = i * TPR + lane;
+      if (c < whole) {
+#pragma unroll
+        for (int b = 0; b < N; b += VN) {
+          typename Vec<T>::type x;
+#pragma unroll
+          for (int e = 0; e < VN; ++e) x[e] = from_f32<T>(v[i][b + e]);
+          *reinterpret_cast<typename Vec<T>::type*>(row + c * N + b) = x;
+        }
+      }
+    }
+    if (whole * N + lane < dim) row[whole * N + lane] = from_f32<T>(rest);
+  }
+};
 
 __device__ __forceinline__ float gate_of(float z, int gate) {
   if (gate == GATE_LINEAR) return z;
@@ -94,53 +137,24 @@ __global__ __launch_bounds__(threads_of<TPR>()) void gated_norm_kernel(GatedNorm
   __shared__ float red[2][NT / 64];
   const int lane = threadIdx.x % TPR, sub = threadIdx.x / TPR;
   const float inv = 1.f / (float)a.dim;
-  float w[NI][N];
-#pragma unroll
-  for (int i = 0; i < NI; ++i) {
-    const int c = (i * TPR + lane) * N;
-    if (a.w) load_cols<float, N>(a.w, c, a.dim, w[i]);
-    else {
-#pragma unroll
-      for (int e = 0; e < N; ++e) w[i][e] = 1.f;
-    }
-  }
+  Columns<NI, N> w, f, g;
+  w.fill(1.f);
+  if (a.w) w.template load<TPR>(a.w, lane, a.dim);
   int par = 0;
   for (int64_t row0 = (int64_t)blockIdx.x * RPB; row0 < a.rows; row0 += (int64_t)gridDim.x * RPB, par ^= 1) {
     const int64_t row = row0 + sub;
     const int dim = row < a.rows ? a.dim : 0;  // a row past the end has no columns
-    const T* x = static_cast<const T*>(a.x) + row * a.xs;
-    const T* z = static_cast<const T*>(a.z) + row * a.zs;
-    float f[NI][N], g[NI][N];
-    float ss = 0.f;
-#pragma unroll
-    for (int i = 0; i < NI; ++i) load_cols<T, N>(x, (i * TPR + lane) * N, dim, f[i]);
+    f.template load<TPR>(static_cast<const T*>(a.x) + row * a.xs, lane, dim);
     if (a.z) {
-#pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        load_cols<T, N>(z, (i * TPR + lane) * N, dim, g[i]);
-#pragma unroll
-        for (int e = 0; e < N; ++e) {
-          g[i][e] = gate_of(g[i][e], a.gate);
-          if (a.gate_first) f[i][e] *= g[i][e];
-        }
-      }
+      g.template load<TPR>(static_cast<const T*>(a.z) + row * a.zs, lane, dim);
+      g.each([&](float& z) { z = gate_of(z, a.gate); });
+      if (a.gate_first) f.with(g, [](float& x, float z) { x *= z; });
     }
-#pragma unroll
-    for (int i = 0; i < NI; ++i)
-#pragma unroll
-      for (int e = 0; e < N; ++e) ss += f[i][e] * f[i][e];
-    ss = row_sum<TPR>(ss, red[par]);
+    const float ss = row_sum<TPR>(f.squares(), red[par]);
     const float rs = __builtin_amdgcn_rsqf(ss * inv + a.eps);
-    T* y = static_cast<T*>(a.y) + row * a.ys;
-#pragma unroll
-    for (int i = 0; i < NI; ++i) {
-#pragma unroll
-      for (int e = 0; e < N; ++e) {
-        f[i][e] = f[i][e] * rs * w[i][e];
-        if (a.z && !a.gate_first) f[i][e] *= g[i][e];
-      }
-      store_cols<T, N>(y, (i * TPR + lane) * N, dim, f[i]);
-    }
+    f.with(w, [&](float& x, float y) { x *= rs * y; });
+    if (a.z && !a.gate_first) f.with(g, [](float& x, float z) { x *= z; });
+    f.template store<TPR>(static_cast<T*>(a.y) + row * a.ys, lane, dim);
   }
 }
 
@@ -150,75 +164,39 @@ __global__ __launch_bounds__(threads_of<TPR>()) void block_norm_kernel(BlockNorm
   __shared__ float red[2][NT / 64];
   const int lane = threadIdx.x % TPR, sub = threadIdx.x / TPR;
   const float inv = 1.f / (float)a.dim;
-  // scale c w_post and w_pre
-  float wp[NI][N], wn[NI][N];
-#pragma unroll
-  for (int i = 0; i < NI; ++i) {
-    const int c = (i * TPR + lane) * N;
-#pragma unroll
-    for (int e = 0; e < N; ++e) wp[i][e] = wn[i][e] = 1.f;
-    if (a.w_post) load_cols<float, N>(a.w_post, c, a.dim, wp[i]);
-    if (a.w_pre) load_cols<float, N>(a.w_pre, c, a.dim, wn[i]);
-    if (a.c) {
-      float f[N];
-      load_cols<float, N>(a.c, c, a.dim, f);
-#pragma unroll
-      for (int e = 0; e < N; ++e) wp[i][e] *= f[e];
-    }
-#pragma unroll
-    for (int e = 0; e < N; ++e) wp[i][e] *= a.scale;
+  Columns<NI, N> wp, wn, f, g, r;  // wp: scale c w_post
+  wp.fill(1.f);
+  if (a.w_post) wp.template load<TPR>(a.w_post, lane, a.dim);
+  if (a.c) {
+    f.template load<TPR>(a.c, lane, a.dim);
+    wp.with(f, [](float& x, float c) { x *= c; });
   }
+  wp.each([&](float& x) { x *= a.scale; });
+  wn.fill(1.f);
+  if (a.w_pre) wn.template load<TPR>(a.w_pre, lane, a.dim);
   int par = 0;
   for (int64_t row0 = (int64_t)blockIdx.x * RPB; row0 < a.rows; row0 += (int64_t)gridDim.x * RPB) {
     const int64_t row = row0 + sub;
     const int dim = row < a.rows ? a.dim : 0;
-    const T* x = static_cast<const T*>(a.x) + row * a.xs;
-    const T* z = static_cast<const T*>(a.z) + row * a.zs;
-    const TR* r = static_cast<const TR*>(a.r) + row * a.rs;
-    float f[NI][N], g[NI][N], res[NI][N];
-#pragma unroll
-    for (int i = 0; i < NI; ++i) load_cols<T, N>(x, (i * TPR + lane) * N, dim, f[i]);
-#pragma unroll
-    for (int i = 0; i < NI; ++i) load_cols<TR, N>(r, (i * TPR + lane) * N, dim, res[i]);
-    if (a.z) {
-#pragma unroll
-      for (int i = 0; i < NI; ++i) load_cols<T, N>(z, (i * TPR + lane) * N, dim, g[i]);
-    }
+    f.template load<TPR>(static_cast<const T*>(a.x) + row * a.xs, lane, dim);
+    r.template load<TPR>(static_cast<const TR*>(a.r) + row * a.rs, lane, dim);
+    if (a.z) g.template load<TPR>(static_cast<const T*>(a.z) + row * a.zs, lane, dim);
     float rs = 1.f;
     if (a.w_post) {
-      float ss = 0.f;
-#pragma unroll
-      for (int i = 0; i < NI; ++i)
-#pragma unroll
-        for (int e = 0; e < N; ++e) ss += f[i][e] * f[i][e];
-      ss = row_sum<TPR>(ss, red[par]);
+      const float ss = row_sum<TPR>(f.squares(), red[par]);
       par ^= 1;
       rs = __builtin_amdgcn_rsqf(ss * inv + a.eps);
     }
-    float ss = 0.f;
-    TR* ro = static_cast<TR*>(a.r_out) + row * a.ros;
-#pragma unroll
-    for (int i = 0; i < NI; ++i) {
-#pragma unroll
-      for (int e = 0; e < N; ++e) {
-        float p = f[i][e] * rs * wp[i][e];
-        if (a.z) p *= gate_of(g[i][e], a.gate);
-        res[i][e] += p;
-        ss += res[i][e] * res[i][e];
-      }
-      store_cols<TR, N>(ro, (i * TPR + lane) * N, dim, res[i]);
-    }
+    f.with(wp, [&](float& x, float y) { x *= rs * y; });
+    if (a.z) f.with(g, [&](float& x, float z) { x *= gate_of(z, a.gate); });
+    r.with(f, [](float& x, float p) { x += p; });
+    r.template store<TPR>(static_cast<TR*>(a.r_out) + row * a.ros, lane, dim);
     if (a.w_pre) {
-      ss = row_sum<TPR>(ss, red[par]);
+      const float ss = row_sum<TPR>(r.squares(), red[par]);
       par ^= 1;
       rs = __builtin_amdgcn_rsqf(ss * inv + a.eps);
-      T* y = static_cast<T*>(a.y) + row * a.ys;
-#pragma unroll
-      for (int i = 0; i < NI; ++i) {
-#pragma unroll
-        for (int e = 0; e < N; ++e) res[i][e] *= rs * wn[i][e];
-        store_cols<T, N>(y, (i * TPR + lane) * N, dim, res[i]);
-      }
+      r.with(wn, [&](float& x, float y) { x *= rs * y; });
+      r.template store<TPR>(static_cast<T*>(a.y) + row * a.ys, lane, dim);
     }
   }
 }
@@ -271,7 +249,8 @@ struct BlockLaunch {
   }
 };
 
-int vectors(int dim, bool bf) { return bf ? (dim + 7) / 8 : (dim + 3) / 4; }
+// Whole vectors of a row; its rest goes one column a thread.
+int vectors(int dim, bool bf) { return bf ? dim / 8 : dim / 4; }
 
 }  // namespace
 
