@@ -9,6 +9,11 @@
 // several rows and keeps its columns' weights in registers.  Vectors need
 // only their elements' alignment (the hardware takes unaligned 16-byte
 // accesses).
+//
+// Bound by the memory: 1 M rows of 128 in bf16 with a gate, 805 MB, 147 us
+// (5.5 TB/s, above a copy's 4.75: two reads to a write); 32,768 rows of 4,096
+// around a block with every option, 1.34 GB, 249 us (5.4 TB/s).  Rows of 4,097,
+// whose vectors are not aligned, run at 4.1 to 4.9 TB/s.
 #include "kda_device.h"
 #include "kda_norm_launch.h"
 
@@ -201,7 +206,9 @@ __global__ __launch_bounds__(threads_of<TPR>()) void block_norm_kernel(BlockNorm
   }
 }
 
-// Threads per row and vectors per thread of a row of `nvec` vectors.
+// Threads per row and vectors per thread of a row of `nvec` vectors: at most two
+// vectors each (a block norm holds five operands of each in registers), four
+// where 1,024 threads do not go round otherwise.
 // (16,384 columns are 2,048 vectors of bf16 and 4,096 of fp32.)
 template <typename T, typename L>
 hipError_t dispatch(int nvec, const L& l) {

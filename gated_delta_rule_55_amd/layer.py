@@ -173,7 +173,7 @@ def linear_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.T
     h0p = None if h0 is None else _dense(h0, "h0", shape, sd, dev)
     with _on(dev, stream):
         if out is None:
-            out = v.new_empty((T, H, dv))
+            out = torch.empty_like(v) if vs == 0 else v.new_empty((T, H, dv))
             op, os_ = out.data_ptr(), 0
         else:
             op, os_ = _rows3(out, "out", (T, H, dv), dt, dev)
@@ -228,7 +228,7 @@ def linear_decode(state: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torc
     decay, gp = _decay(g, N, H, dev)
     with _on(dev, stream):
         if out is None:
-            out = v.new_empty((N, H, dv))
+            out = torch.empty_like(v) if vs == 0 else v.new_empty((N, H, dv))
             op, os_ = out.data_ptr(), 0
         else:
             op, os_ = _rows3(out, "out", (N, H, dv), dt, dev)
@@ -303,7 +303,7 @@ def gated_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
     zp, zs = (0, 0) if gate is None else _rows(gate, "gate", shape, dt, dev)
     with _on(dev, stream):
         if out is None:
-            out = x.new_empty(shape)
+            out = torch.empty_like(x) if xs == 0 else x.new_empty(shape)
             yp, ys = out.data_ptr(), 0
         else:
             yp, ys = _rows(out, "out", shape, dt, dev)
@@ -352,14 +352,14 @@ def block_norm(x: torch.Tensor, residual: torch.Tensor,
         raise ValueError("out needs weight_pre")
     with _on(dev, stream):
         if residual_out is None:
-            residual_out = residual.new_empty(shape)
+            residual_out = torch.empty_like(residual) if rs == 0 else residual.new_empty(shape)
             rop, ros = residual_out.data_ptr(), 0
         else:
             rop, ros = _rows(residual_out, "residual_out", shape, rd, dev)
         yp, ys = 0, 0
         if weight_pre is not None:
             if out is None:
-                out = x.new_empty(shape)
+                out = torch.empty_like(x) if xs == 0 else x.new_empty(shape)
                 yp = out.data_ptr()
             else:
                 yp, ys = _rows(out, "out", shape, dt, dev)
