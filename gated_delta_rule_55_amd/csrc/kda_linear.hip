@@ -259,6 +259,29 @@ struct Smem {
   Decays d[2][HG];                                 // of this chunk and the next
 };
 
+// x of the lane that a data-parallel primitive's control names, 0 where there is
+// none or the row of 16 lanes is not in ROWS.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp(double x) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  const unsigned int lo = __builtin_amdgcn_update_dpp(0, (int)(unsigned int)u, CTRL, ROWS, 0xf, true);
+  const unsigned int hi = __builtin_amdgcn_update_dpp(0, (int)(u >> 32), CTRL, ROWS, 0xf, true);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
+// Inclusive sums over the wave's lanes: within rows of 16 by shifts of 1, 2, 4
+// and 8, then lane 15 of a row to the next one and lane 31 to the upper half.
+// (Through LDS permutes the sums of two heads took longer than a score tile.)
+__device__ __forceinline__ double wave_scan(double x) {
+  x += dpp<0x111, 0xf>(x);
+  x += dpp<0x112, 0xf>(x);
+  x += dpp<0x114, 0xf>(x);
+  x += dpp<0x118, 0xf>(x);
+  x += dpp<0x142, 0xa>(x);
+  x += dpp<0x143, 0xc>(x);
+  return x;
+}
+
 // One wave: the log-decay sums of a chunk and what is made of them.  Sums are
 // fp64, and differences are taken from hi + lo pairs, so that a strong decay
 // in the chunk does not cost the weaker ones after it their digits.  Returns G.
@@ -270,13 +293,11 @@ __device__ __forceinline__ double decay_sums(Decays& d, float g, bool head, int 
     G = (double)g * n;
     all = (double)g * valid;
   } else {
-    G = lane < valid ? (double)g : 0.0;
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-      const double x = __shfl_up(G, off, 64);
-      if (lane >= off) G += x;
-    }
-    all = __shfl(G, 63, 64);
+    G = wave_scan(lane < valid ? (double)g : 0.0);
+    const uint64_t u = __builtin_bit_cast(uint64_t, G);
+    const unsigned int lo = __builtin_amdgcn_readlane((int)(unsigned int)u, 63);
+    const unsigned int hi = __builtin_amdgcn_readlane((int)(u >> 32), 63);
+    all = __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
   }
   constexpr double kL2E = 1.4426950408889634074;
   const double G2 = G * kL2E;
