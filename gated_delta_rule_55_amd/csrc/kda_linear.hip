@@ -711,7 +711,7 @@ int64_t linear_segment(int64_t t_total, int n_seqs, int n_heads, int dv, bool bf
   // sequence of 32,768 tokens x 32 heads: 400 us, with twelve 455, sixteen 424);
   // for several sequences, whose segments are not equally long, twelve (eight of
   // 33,001 tokens in all: 395 us, with eight or sixteen 455 to 460)
-  const int64_t waves = n_seqs == 1 ? 2048 : 3072;
+  const int64_t waves = 256 * (n_seqs == 1 ? 8 : 12);
   const int64_t want = (t_total * n_heads * (dv / 32) + waves - 1) / waves;
   const int64_t seg = (want + C - 1) / C * C;
   // below that a split costs two launches more: taken for short sequences only
