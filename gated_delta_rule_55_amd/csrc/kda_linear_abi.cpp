@@ -19,6 +19,8 @@ using kda::range_of;
 using kda::row_set;
 using kda::RowSet;
 
+// Workgroups of a launch: 256 threads each stay below 2^32.
+constexpr int64_t kMaxBlocks = (int64_t)1 << 24;
 constexpr int64_t kMaxStride = (int64_t)1 << 22;
 // (slot, head) states of a pool: keeps its size in bytes in 64 bits.
 constexpr int64_t kMaxStates = (int64_t)1 << 40;
@@ -71,8 +73,8 @@ int check_linear(const kda_linear_prefill_desc* d, kda::LinearPrefillArgs* a) {
   a->scale = d->scale != 0.f ? d->scale : 1.0f / std::sqrt((float)d->dk);
   // workgroups: segments x heads, and 8 per segment length and head that join them
   const int64_t seg = kda::linear_segment(a->t_total, a->n_seqs, a->n_heads, a->dv, a->bf16);
-  if ((kda::linear_segments(a->t_total, a->n_seqs, seg) + 8) * H > INT32_MAX ||
-      a->t_total / seg * H * 8 > INT32_MAX)
+  if ((kda::linear_segments(a->t_total, a->n_seqs, seg) + 8) * H >= kMaxBlocks ||
+      a->t_total / seg * H * 8 >= kMaxBlocks)
     return KDA_ERR_SHAPE;
   return KDA_OK;
 }
@@ -161,7 +163,7 @@ int kda_linear_decode(const kda_linear_decode_desc* d, void* stream) {
       (st = check_stride(d->v_stride, H * d->dv, es, &a.v_stride)) != KDA_OK ||
       (st = check_stride(d->o_stride, H * d->dv, es, &a.o_stride)) != KDA_OK)
     return st;
-  if (N * H * 4 > INT32_MAX) return KDA_ERR_SHAPE;  // up to dv / 32 workgroups per (sequence, head)
+  if (N * H >= kMaxBlocks) return KDA_ERR_SHAPE;
   if (N == 0) return KDA_OK;
   if (!d->state || !d->q || !d->k || !d->v || !d->g || !d->o) return KDA_ERR_NULL;
   const void* p16[] = {d->state, d->q, d->k, d->v, d->o};

@@ -130,7 +130,8 @@ def linear_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.T
     v: [T, H, dv]; dk and dv each 32, 64 or 128; fp32 or bf16.  g: fp32
     log-decays [T, H], or [H] for one constant decay per head.  h0:
     [N, H, dk, dv] fp32 (or bf16 with bf16 inputs) or None; cu_seqlens: int32
-    [N + 1] on the device or None (one sequence); scale: dk^-1/2 by default.
+    [N + 1] on the device or None (one sequence); scale: dk^-1/2 by default (and
+    for 0).
     Returns (o [T, H, dv], ht [N, H, dk, dv] or None); ht may be h0 itself
     (in-place carry).  q, k, v and out may be slices of wider buffers: only
     their first stride may differ from a dense tensor's (a multiple of 16

@@ -64,7 +64,8 @@ typedef enum { KDA_DECAY_TOKEN = 0, KDA_DECAY_HEAD = 1 } kda_decay;
 typedef struct {
   uint32_t struct_size;         /* sizeof(kda_linear_prefill_desc)              */
   int32_t dtype;                /* kda_dtype of q, k, v, o                      */
-  int32_t n_seqs;               /* N >= 1                                       */
+  int32_t n_seqs;               /* N >= 1; a call's N * H (and its segments)    */
+                                /* stay below 2^24                              */
   int32_t n_heads;              /* H, 1 .. 65535                                */
   int32_t n_k_heads;            /* Hk, dividing H; 0 = H                        */
   int32_t dk, dv;               /* each in {32, 64, 128}                        */
@@ -97,7 +98,7 @@ typedef struct {
 typedef struct {
   uint32_t struct_size;         /* sizeof(kda_linear_decode_desc)               */
   int32_t dtype;                /* kda_dtype of q, k, v, o                      */
-  int32_t n_seqs;               /* N >= 0 (0 = nothing to do)                   */
+  int32_t n_seqs;               /* N >= 0 (0 = nothing to do); N * H < 2^24     */
   int32_t n_heads;              /* H, 1 .. 65535                                */
   int32_t n_k_heads;            /* Hk, dividing H; 0 = H                        */
   int32_t dk, dv;               /* each in {32, 64, 128}                        */

@@ -386,3 +386,39 @@ def test_prefill_heads_sharing_a_key_head(kda, H, Hk, dk, dv, dtype):
     i = linear_inputs(24, [500, 3, 0, 90], H, Hk, dk, dv, dtype, g_scale=0.2)
     o, ht = run(kda, cuda(i))
     check_linear(i, o, ht)
+
+
+def test_two_streams_at_once(kda):
+    """Calls in flight on two streams, each with a workspace of its own: the
+    results of either alone, bit for bit."""
+    sets = [cuda(linear_inputs(s, [1500, 700], 4, 4, 128, 128, BF, g_scale=0.05)) for s in (25, 26)]
+    want = [run(kda, d) for d in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    for _ in range(5):
+        got = []
+        for d, s in zip(sets, streams):
+            got.append(run(kda, d, stream=s))
+        torch.cuda.synchronize()
+        for (o, ht), (wo, wh) in zip(got, want):
+            assert torch.equal(o, wo) and torch.equal(ht, wh)
+
+
+def test_pools_given_one_way_only(kda):
+    """A pool to read from without one to write to, and the reverse."""
+    i = linear_inputs(27, [20, 150], 2, 2, 32, 64, BF, n_states=4)
+    d = cuda(i)
+    idx = torch.tensor([3, 1], dtype=torch.int32, device="cuda")
+    part = dict(i, h0=i["h0"][[3, 1]].contiguous())
+    before = d["h0"].clone()
+    o, none = run(kda, d, state_indices=idx, output_final_state=False)
+    assert none is None and torch.equal(d["h0"], before)
+    check_linear(part, o, None)
+    pool = torch.full_like(d["h0"], 6.0)
+    o, ht = kda.linear_prefill(d["q"], d["k"], d["v"], d["g"], None, d["cu"], ht=pool, state_indices=idx)
+    assert ht is pool and torch.all(pool[0] == 6.0) and torch.all(pool[2] == 6.0)
+    check_linear(dict(i, h0=None), o, pool[[3, 1]])
+    both = torch.full_like(d["h0"], 6.0)
+    o, ht = run(kda, d, ht=both, state_indices=idx)
+    assert torch.equal(d["h0"], before)
+    check_linear(part, o, both[[3, 1]])

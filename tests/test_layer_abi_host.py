@@ -61,7 +61,7 @@ def _prefill(al, over):
     (dict(n_k_heads=8), -2), (dict(dk=96), -4), (dict(dv=256), -4), (dict(decay=2), -4),
     (dict(t_total=-1), -2), (dict(t_total=1 << 31), -2), (dict(scale=float("nan")), -2),
     (dict(state_dtype=9), -3), (dict(dtype=1, state_dtype=2), -4),
-    (dict(n_seqs=600_000_000), -2),                                 # workgroups past 32 bits
+    (dict(n_seqs=1 << 22), -2),                                     # threads of a launch past 32 bits
     (dict(q_stride=64), -2), (dict(k_stride=132), -2), (dict(v_stride=1 << 29), -2),
     (dict(o_stride=-8), -2),
     (dict(state_indices=0x8000000, n_slots=0), -2),
@@ -109,7 +109,7 @@ def test_linear_workspace(al):
     (dict(struct_size=8), -8), (dict(dtype=5), -3), (dict(n_seqs=-1), -2), (dict(n_heads=0), -2),
     (dict(n_k_heads=3), -2), (dict(dk=16), -4), (dict(dv=0), -4), (dict(decay=-1), -4),
     (dict(scale=float("inf")), -2), (dict(state_dtype=4), -3), (dict(dtype=1, state_dtype=2), -4),
-    (dict(n_seqs=1 << 28), -2), (dict(q_stride=100), -2), (dict(state_indices=0x8000000, n_slots=-1), -2),
+    (dict(n_seqs=1 << 22), -2), (dict(q_stride=100), -2), (dict(state_indices=0x8000000, n_slots=-1), -2),
     (dict(state=None), -1), (dict(v=None), -1), (dict(g=None), -1), (dict(k=0x2000008), -5),
     (dict(state=0x6000008), -5), (dict(g=0x4000001), -5), (dict(o=0x6000000), -9),
     (dict(o=0x3000000), -9), (dict(state=0x2000000), -9), (dict(n_seqs=0, state=None, q=None), 0),
