@@ -1,4 +1,5 @@
-"""Build libkda.so (HIP kernels + C ABI) for gfx950 with hipcc, in-tree.
+"""Build libkda.so (HIP kernels + C ABI) for gfx950 with hipcc, and the Python
+module _fast.so on top of it, in-tree.
 
 Usage: python -m gated_delta_rule_55_amd.build [-v]
 """
@@ -34,6 +35,28 @@ HIPCC_FLAGS = [
 SOURCE_FLAGS = {
     "kda_prefill.hip": ["-mllvm", "-amdgpu-sched-strategy=iterative-ilp"],
 }
+
+
+# The Python module that marshals the layer calls (csrc/kda_torch.cpp): host code
+# against torch's headers, on top of libkda.so.
+FAST_OUT = os.path.join(PKG, "_fast.so")
+
+
+def _fast_command():
+    import sysconfig
+
+    import torch
+
+    troot = os.path.dirname(torch.__file__)
+    rocm = os.environ.get("ROCM_PATH", "/opt/rocm")
+    include = [f"-I{INCLUDE}"] + [f"-isystem{d}" for d in (
+        os.path.join(troot, "include"), os.path.join(troot, "include", "torch", "csrc", "api", "include"),
+        os.path.join(rocm, "include"), sysconfig.get_paths()["include"])]
+    return (["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-Werror", "-D__HIP_PLATFORM_AMD__",
+             "-DUSE_ROCM", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"] + include +
+            [os.path.join(CSRC, "kda_torch.cpp"), "-o", FAST_OUT + ".tmp",
+             f"-L{os.path.join(troot, 'lib')}", "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_python",
+             f"-L{PKG}", "-l:libkda.so", "-Wl,-rpath,$ORIGIN"])
 
 
 def _hipcc():
@@ -74,6 +97,11 @@ def build(verbose: bool = False, jobs: int = 4) -> str:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
     os.replace(OUT + ".tmp", OUT)
+    cmd = _fast_command()
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True)
+    os.replace(FAST_OUT + ".tmp", FAST_OUT)
     if verbose:
         print(f"built {OUT} in {time.time() - t0:.1f}s", flush=True)
     return OUT

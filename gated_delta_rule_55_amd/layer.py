@@ -4,6 +4,11 @@ argument marshalling only, as kda.py does for the KDA step.
 
 Calls run on the device of their tensors, on `stream` or that device's current
 stream; outputs and workspaces made here are allocated for that stream.
+
+A call with dense tensors on the current device and stream goes through the
+module _fast (csrc/kda_torch.cpp), which checks and launches it in 1 us above the
+launch itself; it answers None to every other call, and to one that it would
+have to refuse, which is then checked here, and made or refused.
 """
 from __future__ import annotations
 
@@ -15,6 +20,11 @@ import torch
 
 from . import _abi
 from . import _abi_layer as _al
+
+try:
+    from . import _fast
+except ImportError:  # not built: every call is checked and made here
+    _fast = None
 
 _DTYPES = {torch.float32: _abi.KDA_DTYPE_F32, torch.bfloat16: _abi.KDA_DTYPE_BF16}
 
@@ -142,6 +152,12 @@ def linear_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.T
     (a captured graph keeps its own); allocated here when None.
     cu_seqlens is read on the device: contents that break its rules give
     unspecified results but no access out of bounds."""
+    if _fast is not None and stream is None and (
+            state_dtype is None or (h0 is None and ht is None and state_dtype in _DTYPES)):
+        done = _fast.linear_prefill(q, k, v, g, h0, cu_seqlens, scale, out, ht, workspace,
+                                    output_final_state, state_indices, state_dtype == torch.bfloat16)
+        if done is not None:
+            return done
     dev, dt = _linear_common("linear_prefill", q, v)
     T, Hk, dk = q.shape
     H, dv = v.shape[1], v.shape[2]
@@ -211,6 +227,10 @@ def linear_decode(state: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torc
     pool [S, H, dk, dv] and sequence n updates slot state_indices[n]; a
     negative slot skips it (its o is left as it was).  Strides as in
     linear_prefill."""
+    if _fast is not None and stream is None:
+        done = _fast.linear_decode(state, q, k, v, g, scale, out, state_indices)
+        if done is not None:
+            return done
     dev, dt = _linear_common("linear_decode", q, v)
     N, Hk, dk = q.shape
     H, dv = v.shape[1], v.shape[2]
@@ -297,6 +317,10 @@ def gated_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
     (ones); gate as x, or None for the plain norm; activation None, "silu" or
     "sigmoid".  Rows may lie at any one stride.  out may be x or gate itself.
     Sums and everything up to the result's rounding are fp32."""
+    if _fast is not None and stream is None:
+        done = _fast.gated_norm(x, weight, gate, activation, gate_first, eps, out)
+        if done is not None:
+            return done
     dev, dt, dim = _norm_common("gated_norm", x, activation)
     shape = x.shape
     xp, xs = _rows(x, "x", shape, dt, dev)
@@ -338,6 +362,11 @@ def block_norm(x: torch.Tensor, residual: torch.Tensor,
     with bf16 x; weights fp32 [dim].  y comes from r before r is rounded.
     residual_out may be residual itself; out may be x or gate itself.  Rows may
     lie at any one stride."""
+    if _fast is not None and stream is None:
+        done = _fast.block_norm(x, residual, weight_post, weight_pre, gate, activation, channel_scale,
+                                scale, eps, residual_out, out)
+        if done is not None:
+            return done
     dev, dt, dim = _norm_common("block_norm", x, activation)
     shape = x.shape
     rd = residual.dtype if isinstance(residual, torch.Tensor) else None
