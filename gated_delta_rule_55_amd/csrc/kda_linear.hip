@@ -1,7 +1,7 @@
 // kda_linear.hip -- linear attention with one decay per head over packed
 // sequences (kda_linear_prefill).
 //
-// In chunks of 64 tokens, with G_i the sum of the log-decays of a chunk's
+// In chunks of 64 tokens (32 in fp32), with G_i the sum of the log-decays of a chunk's
 // tokens up to and with i, G the whole chunk's and S the state before it:
 //     o_i = scale (exp(G_i) S^T q_i + sum_{j <= i} exp(G_i - G_j) (q_i . k_j) v_j)
 //     S  <- exp(G) S + sum_j exp(G - G_j) k_j v_j^T
@@ -41,7 +41,7 @@
 namespace kda {
 namespace {
 
-constexpr int C = 64;          // tokens per chunk
+constexpr int kGrain = 64;       // segments are multiples of this many tokens
 constexpr float kMinG = -200.f;  // exp(-200) is 0 in fp32: -inf becomes a finite sum
 
 struct LinearParams {
@@ -90,7 +90,7 @@ __device__ __forceinline__ int count_segments(const LinearParams& P, int len, in
   each = P.L;
   if (len <= P.L) return 1;
   const unsigned int most = div_l(P, len - 1) + 1;
-  each = (int)(((unsigned int)len + most - 1) / most + C - 1) / C * C;
+  each = (int)(((unsigned int)len + most - 1) / most + kGrain - 1) / kGrain * kGrain;
   return (int)(((unsigned int)len + each - 1) / (unsigned int)each);
 }
 
@@ -216,7 +216,7 @@ __device__ __forceinline__ void store_state(const f32x16 (&S)[KT], TS* p, int la
 // vectors.  Loads go through a buffer resource that ends with the chunk's last
 // row, so rows past it read as zeros without a branch, and a thread's offsets
 // are the same for every chunk.
-template <typename T, int D, int NT>
+template <typename T, int C, int D, int NT>
 struct Rows {
   static constexpr int VE = 16 / sizeof(T);      // elements per vector
   static constexpr int VPR = D / VE;             // vectors per row
@@ -243,6 +243,7 @@ struct Rows {
 };
 
 // The decays of a chunk's tokens for one head, in powers of two.
+template <int C>
 struct Decays {
   alignas(16) float ghi[C], glo[C];  // G_i as a sum of two floats
   alignas(16) float eg[C], ed[C];    // exp(G_i), exp(G - G_i)
@@ -250,13 +251,14 @@ struct Decays {
 };
 
 // LDS of a workgroup: VW value columns (HG heads of VW / HG).
-template <typename T, int DK, int VW, int HG, bool OUT>
+template <typename T, int C, int DK, int VW, int HG, bool OUT>
 struct Smem {
-  alignas(16) T k[C * Rows<T, DK, 64>::S];
-  alignas(16) T v[C * Rows<T, VW, 64>::S];
-  alignas(16) T q[OUT ? C * Rows<T, DK, 64>::S : 8];
-  alignas(16) T p[OUT ? HG * 3 * 2 * 64 * 8 : 8];  // score tiles as B operands
-  Decays d[2][HG];                                 // of this chunk and the next
+  static constexpr int TILES = C / 32 * (C / 32 + 1) / 2;  // score tiles of a head
+  alignas(16) T k[C * Rows<T, C, DK, 2 * VW>::S];
+  alignas(16) T v[C * Rows<T, C, VW, 2 * VW>::S];
+  alignas(16) T q[OUT ? C * Rows<T, C, DK, 2 * VW>::S : 8];
+  alignas(16) T p[OUT ? HG * TILES * 2 * 64 * 8 : 8];  // score tiles as B operands
+  Decays<C> d[2][HG];                                  // of this chunk and the next
 };
 
 // x of the lane that a data-parallel primitive's control names, 0 where there is
@@ -285,7 +287,8 @@ __device__ __forceinline__ double wave_scan(double x) {
 // One wave: the log-decay sums of a chunk and what is made of them.  Sums are
 // fp64, and differences are taken from hi + lo pairs, so that a strong decay
 // in the chunk does not cost the weaker ones after it their digits.  Returns G.
-__device__ __forceinline__ double decay_sums(Decays& d, float g, bool head, int valid, int lane) {
+template <int C>
+__device__ __forceinline__ double decay_sums(Decays<C>& d, float g, bool head, int valid, int lane) {
   g = g < kMinG ? kMinG : g;
   double G, all;
   if (head) {
@@ -302,10 +305,12 @@ __device__ __forceinline__ double decay_sums(Decays& d, float g, bool head, int 
   constexpr double kL2E = 1.4426950408889634074;
   const double G2 = G * kL2E;
   const float hi = (float)G2;
-  d.ghi[lane] = hi;
-  d.glo[lane] = (float)(G2 - (double)hi);
-  d.eg[lane] = fast_exp2(hi);
-  d.ed[lane] = fast_exp2((float)((all - G) * kL2E));
+  if (lane < C) {
+    d.ghi[lane] = hi;
+    d.glo[lane] = (float)(G2 - (double)hi);
+    d.eg[lane] = fast_exp2(hi);
+    d.ed[lane] = fast_exp2((float)((all - G) * kL2E));
+  }
   if (lane == 0) d.total = fast_exp2((float)(all * kL2E));
   return all;
 }
@@ -315,13 +320,16 @@ __device__ __forceinline__ double decay_sums(Decays& d, float g, bool head, int 
 // 64 sequences of 1,024 tokens, heads of 128 x 64, eight to a key head: 250 us
 // with two heads a workgroup and the four workgroups of a key head on one XCD,
 // 272 with them spread, 477 with one head a workgroup.
-template <typename T, int DK, int VW, int HG, bool OUT>
-__global__ __launch_bounds__(2 * VW, sizeof(T) == 2 && VW == 128 && HG < 4 ? 2 : 1) void linear_kernel(LinearParams P) {
+template <typename T, int C, int DK, int VW, int HG, bool OUT>
+__global__ __launch_bounds__(2 * VW, sizeof(T) != 2 || VW != 128 || HG == 4 ? 1 : 2)
+void linear_kernel(LinearParams P) {
   constexpr int NW = VW / 32, NT = 64 * NW, KT = DK / 32, DV = VW / HG;
-  using RQ = Rows<T, DK, NT>;
-  using RV = Rows<T, VW, NT>;
+  constexpr int TT = C / 32;  // 32-token tiles of a chunk
+  using RQ = Rows<T, C, DK, NT>;
+  using RV = Rows<T, C, VW, NT>;
   using F = typename Frag<T>::type;
-  __shared__ Smem<T, DK, VW, HG, OUT> sm;
+  using SM = Smem<T, C, DK, VW, HG, OUT>;
+  __shared__ SM sm;
 
   const int groups = P.H / HG;
   int id, group;
@@ -369,7 +377,7 @@ __global__ __launch_bounds__(2 * VW, sizeof(T) == 2 && VW == 128 && HG < 4 ? 2 :
   auto fetch_g = [&](int c0) {
 #pragma unroll
     for (int x = 0; x < HG; ++x)
-      g[x] = P.decay_head ? P.g[hb + x] : lane < len - c0 ? P.g[(int64_t)(s.begin + c0 + lane) * P.H + hb + x] : 0.f;
+      g[x] = P.decay_head ? P.g[hb + x] : lane < valid_at(c0) ? P.g[(int64_t)(s.begin + c0 + lane) * P.H + hb + x] : 0.f;
   };
   auto sum_g = [&](int c0, int b) {
 #pragma unroll
@@ -409,15 +417,15 @@ __global__ __launch_bounds__(2 * VW, sizeof(T) == 2 && VW == 128 && HG < 4 ? 2 :
         fetch_g(c0 + 2 * C);
       }
     }
-    const Decays& dw = sm.d[buf][hw];
+    const Decays<C>& dw = sm.d[buf][hw];
 
-    f32x16 O[2];
+    f32x16 O[TT];
     if (OUT) {
       // scores^T of tile (jt, it): rows = keys j, columns = queries i
 #pragma unroll
-      for (int tt = 0; tt < (3 + NW - 1) / NW; ++tt) {
+      for (int tt = 0; tt < (SM::TILES + NW - 1) / NW; ++tt) {
         const int tile = w + tt * NW;
-        if (tile >= 3) break;
+        if (tile >= SM::TILES) break;
         const int jt = tile >> 1, it = (tile + 1) >> 1;
         f32x16 a;
 #pragma unroll
@@ -429,7 +437,7 @@ __global__ __launch_bounds__(2 * VW, sizeof(T) == 2 && VW == 128 && HG < 4 ? 2 :
         const int i = 32 * it + col;
 #pragma unroll
         for (int hx = 0; hx < HG; ++hx) {
-          const Decays& d = sm.d[buf][hx];
+          const Decays<C>& d = sm.d[buf][hx];
           const float hi = d.ghi[i], lo = d.glo[i];
           f32x16 b;
 #pragma unroll
@@ -445,12 +453,12 @@ __global__ __launch_bounds__(2 * VW, sizeof(T) == 2 && VW == 128 && HG < 4 ? 2 :
           }
 #pragma unroll
           for (int x = 0; x < 2; ++x)
-            store_frag8(sm.p + ((hx * 6 + tile * 2 + x) * 64 + lane) * 8, frag_of_d<T>(b, x));
+            store_frag8(sm.p + (((hx * SM::TILES + tile) * 2 + x) * 64 + lane) * 8, frag_of_d<T>(b, x));
         }
       }
       // O^T = S^T Q^T, then the decay since the chunk's start and the scale
 #pragma unroll
-      for (int it = 0; it < 2; ++it)
+      for (int it = 0; it < TT; ++it)
 #pragma unroll
         for (int r = 0; r < 16; ++r) O[it][r] = 0.f;
 #pragma unroll
@@ -459,11 +467,11 @@ __global__ __launch_bounds__(2 * VW, sizeof(T) == 2 && VW == 128 && HG < 4 ? 2 :
         for (int x = 0; x < 2; ++x) {
           const F sf = frag_of_d<T>(S[t], x);
 #pragma unroll
-          for (int it = 0; it < 2; ++it)
+          for (int it = 0; it < TT; ++it)
             O[it] = mma(sf, load_frag8<T>(sm.q + (32 * it + col) * RQ::S + 32 * t + 16 * x + 8 * half), O[it]);
         }
 #pragma unroll
-      for (int it = 0; it < 2; ++it) {
+      for (int it = 0; it < TT; ++it) {
         const float e = dw.eg[32 * it + col] * P.scale;
 #pragma unroll
         for (int r = 0; r < 16; ++r) O[it][r] *= e;
@@ -471,7 +479,7 @@ __global__ __launch_bounds__(2 * VW, sizeof(T) == 2 && VW == 128 && HG < 4 ? 2 :
     }
 
     // S = exp(G) S + K^T V'
-    F vf[4];
+    F vf[2 * TT];
     float poison = 0.f;  // NaN where a value is not finite
     const float total = dw.total;
 #pragma unroll
@@ -479,7 +487,7 @@ __global__ __launch_bounds__(2 * VW, sizeof(T) == 2 && VW == 128 && HG < 4 ? 2 :
 #pragma unroll
       for (int r = 0; r < 16; ++r) S[t][r] *= total;
 #pragma unroll
-    for (int x = 0; x < 4; ++x) {
+    for (int x = 0; x < 2 * TT; ++x) {
       vf[x] = frag_t<false>(sm.v + 16 * x * RV::S + 32 * w, RV::S, lane);
       poison = add_nonfinite(vf[x], poison);
       const f32x4 d0 = *reinterpret_cast<const f32x4*>(dw.ed + 16 * x + 4 * half);
@@ -511,14 +519,14 @@ __global__ __launch_bounds__(2 * VW, sizeof(T) == 2 && VW == 128 && HG < 4 ? 2 :
       const bool bad = __any(poison != 0.f);
       if (bad) {  // a masked score of 0 would turn these into NaN: added below
 #pragma unroll
-        for (int x = 0; x < 4; ++x)
+        for (int x = 0; x < 2 * TT; ++x)
 #pragma unroll
           for (int e = 0; e < 8; ++e)
             if (!finite1(to_f32(vf[x][e]))) vf[x][e] = from_f32<T>(0.f);
       }
-      const T* pw = sm.p + hw * 6 * 64 * 8;
+      const T* pw = sm.p + hw * SM::TILES * 2 * 64 * 8;
 #pragma unroll
-      for (int tile = 0; tile < 3; ++tile) {
+      for (int tile = 0; tile < SM::TILES; ++tile) {
         const int jt = tile >> 1, it = (tile + 1) >> 1;
 #pragma unroll
         for (int x = 0; x < 2; ++x)
@@ -531,16 +539,16 @@ __global__ __launch_bounds__(2 * VW, sizeof(T) == 2 && VW == 128 && HG < 4 ? 2 :
           const T* vrow = vb + (int64_t)(c0 + j) * P.vs + 32 * w;
           const int jt = j >> 5, x = (j >> 4) & 1, jj = j & 15;
           const int e = (jj & 3) + 4 * (jj >> 3), jlane = 32 * ((jj >> 2) & 1) + col;
-          float pj[2];  // P[i][j] of this lane's two queries
+          float pj[TT];  // P[i][j] of this lane's two queries
 #pragma unroll
-          for (int it = 0; it < 2; ++it)
+          for (int it = 0; it < TT; ++it)
             pj[it] = jt <= it ? to_f32(pw[(((jt + it) * 2 + x) * 64 + jlane) * 8 + e]) : 0.f;
 #pragma unroll
           for (int r = 0; r < 16; ++r) {
             const float x1 = to_f32(vrow[d_row(r, half)]);
             if (!finite1(x1)) {
 #pragma unroll
-              for (int it = 0; it < 2; ++it)
+              for (int it = 0; it < TT; ++it)
                 if (32 * it + col >= j) O[it][r] += pj[it] * x1;
             }
           }
@@ -548,7 +556,7 @@ __global__ __launch_bounds__(2 * VW, sizeof(T) == 2 && VW == 128 && HG < 4 ? 2 :
       }
       // lane: token 32 it + col, value columns 8 (r / 4) + 4 half + r % 4
 #pragma unroll
-      for (int it = 0; it < 2; ++it) {
+      for (int it = 0; it < TT; ++it) {
         const int i = 32 * it + col;
         T* op = static_cast<T*>(P.o) + (int64_t)(s.begin + c0 + i) * P.os + hb * DV + 32 * w;
         if constexpr (sizeof(T) == 2) {
@@ -657,12 +665,18 @@ __global__ __launch_bounds__(256) void linear_join_kernel(LinearParams P, int el
   for (int x = 0; x < X; ++x) *reinterpret_cast<f32x4*>(p + 4 * x) = S[x];
 }
 
+// Tokens per chunk.  fp32 takes twice the LDS and registers a token: with 64 its
+// workgroups leave a SIMD one wave, of heads of 128 x 32 even a CU (8,192 tokens
+// x 32 heads: 554 us against 182).
+template <typename T>
+constexpr int kChunk = sizeof(T) == 2 ? 64 : 32;
+
 template <typename T, int DK, int DV, int HG>
 hipError_t launch(const LinearParams& p, bool split, hipStream_t stream) {
   const int64_t blocks = placed_blocks(linear_segments(p.T, p.N, p.L), p.H / HG, p.rep / HG);
   constexpr int VW = DV * HG;
   if (split) {
-    linear_kernel<T, DK, VW, HG, false><<<(unsigned)blocks, 2 * VW, 0, stream>>>(p);
+    linear_kernel<T, kChunk<T>, DK, VW, HG, false><<<(unsigned)blocks, 2 * VW, 0, stream>>>(p);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     constexpr int parts = DK * DV / 1024, parts2 = (parts + 1) / 2;
@@ -675,7 +689,7 @@ hipError_t launch(const LinearParams& p, bool split, hipStream_t stream) {
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  linear_kernel<T, DK, VW, HG, true><<<(unsigned)blocks, 2 * VW, 0, stream>>>(p);
+  linear_kernel<T, kChunk<T>, DK, VW, HG, true><<<(unsigned)blocks, 2 * VW, 0, stream>>>(p);
   return hipGetLastError();
 }
 
@@ -713,12 +727,12 @@ int64_t linear_segment(int64_t t_total, int n_seqs, int n_heads, int dv, bool bf
   // 33,001 tokens in all: 395 us, with eight or sixteen 455 to 460)
   const int64_t waves = 256 * (n_seqs == 1 ? 8 : 12);
   const int64_t want = (t_total * n_heads * (dv / 32) + waves - 1) / waves;
-  const int64_t seg = (want + C - 1) / C * C;
+  const int64_t seg = (want + kGrain - 1) / kGrain * kGrain;
   // below that a split costs two launches more: taken for short sequences only
   // when they alone leave CUs idle (512 tokens x 32 heads in bf16: 31 us against
   // 32 in one segment, 1,024: 36 against 59), and not for 256 tokens (26 against
-  // 19; in fp32, whose chunks take twice as long, 36 against 42)
-  const int64_t least = (int64_t)n_seqs * n_heads >= 256 ? 1024 : bf16 && t_total <= 256 ? 256 : 128;
+  // 19; in fp32, whose products take longer, 24 against 42 for 16 heads of 64)
+  const int64_t least = (int64_t)n_seqs * n_heads >= 256 ? 1024 : !bf16 ? 64 : t_total <= 256 ? 256 : 128;
   return seg < least ? least : seg;
 }
 
