@@ -221,9 +221,9 @@ struct Rows {
   static constexpr int VE = 16 / sizeof(T);      // elements per vector
   static constexpr int VPR = D / VE;             // vectors per row
   static constexpr int RPP = NT / VPR;           // rows per step of the workgroup
-  static constexpr int NV = C / RPP;
+  static constexpr int NV = C / RPP > 0 ? C / RPP : 1;
   static constexpr int S = D + 32 / sizeof(T);   // LDS row stride: 32 bytes of padding
-  static_assert(NT % VPR == 0 && C % RPP == 0, "row tiling");
+  static_assert(NT % VPR == 0 && (C % RPP == 0 || RPP == 2 * C), "row tiling");
   uint4 r[NV];
   static __device__ __forceinline__ int offset(int tid, int64_t stride) {
     return ((tid / VPR) * (int)stride + (tid % VPR) * VE) * (int)sizeof(T);
@@ -236,6 +236,7 @@ struct Rows {
       r[i] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(rs, off + i * RPP * stride * (int)sizeof(T), 0, 0));
   }
   __device__ __forceinline__ void store(T* lds, int tid) const {
+    if (RPP > C && tid / VPR >= C) return;
     T* p = lds + (tid / VPR) * S + (tid % VPR) * VE;
 #pragma unroll
     for (int i = 0; i < NV; ++i) *reinterpret_cast<uint4*>(p + i * RPP * S) = r[i];
@@ -321,7 +322,7 @@ __device__ __forceinline__ double decay_sums(Decays<C>& d, float g, bool head, i
 // with two heads a workgroup and the four workgroups of a key head on one XCD,
 // 272 with them spread, 477 with one head a workgroup.
 template <typename T, int C, int DK, int VW, int HG, bool OUT>
-__global__ __launch_bounds__(2 * VW, sizeof(T) != 2 || VW != 128 || HG == 4 ? 1 : 2)
+__global__ __launch_bounds__(2 * VW, sizeof(T) != 2 || VW != 128 || HG == 4 ? 1 : C == 32 ? 3 : 2)
 void linear_kernel(LinearParams P) {
   constexpr int NW = VW / 32, NT = 64 * NW, KT = DK / 32, DV = VW / HG;
   constexpr int TT = C / 32;  // 32-token tiles of a chunk
@@ -688,6 +689,16 @@ hipError_t launch(const LinearParams& p, bool split, hipStream_t stream) {
       linear_join_kernel<2><<<(unsigned)(most * parts2), 256, 0, stream>>>(p, DK * DV, parts2, marks);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
+  }
+  // Sequences of few tokens in bf16 are mostly loads and stores of states: chunks
+  // of 32 leave room for three workgroups a CU (24 sequences of 851 tokens in all,
+  // 32 heads of 128: 20 us against 24).  Longer ones lose a little by it (64 x
+  // 1,024 tokens: 267 us against 256).
+  if constexpr (sizeof(T) == 2) {
+    if (!split && p.T <= 64 * (int64_t)p.N) {
+      linear_kernel<T, 32, DK, VW, HG, true><<<(unsigned)blocks, 2 * VW, 0, stream>>>(p);
+      return hipGetLastError();
+    }
   }
   linear_kernel<T, kChunk<T>, DK, VW, HG, true><<<(unsigned)blocks, 2 * VW, 0, stream>>>(p);
   return hipGetLastError();

@@ -422,3 +422,16 @@ def test_pools_given_one_way_only(kda):
     o, ht = run(kda, d, ht=both, state_indices=idx)
     assert torch.equal(d["h0"], before)
     check_linear(part, o, both[[3, 1]])
+
+
+@pytest.mark.parametrize("dk,dv,Hk", [(32, 32, 4), (32, 128, 4), (64, 64, 2), (128, 32, 1), (128, 64, 2), (128, 128, 4), (64, 128, 2)])
+def test_prefill_few_tokens_per_sequence(kda, dk, dv, Hk):
+    """Continuing prefills: at most 64 tokens a sequence on average, one of them longer."""
+    i = linear_inputs(28, [1, 31, 32, 33, 0, 64, 65, 127, 5, 2], 4, Hk, dk, dv, BF, state_dtype=BF)
+    o, ht = run(kda, cuda(i))
+    check_linear(i, o, ht)
+    b = dict(i, v=i["v"].clone())
+    b["v"][40, 1, 3] = float("inf")  # in the third sequence
+    o2, h2 = run(kda, cuda(b))
+    assert torch.equal(o2[:40], o[:40]) and torch.equal(o2[64:], o[64:]) and torch.equal(h2[3:], ht[3:])
+    assert torch.isinf(o2[40:64, 1, 3]).any() or torch.isnan(o2[40:64, 1, 3]).any()
