@@ -204,3 +204,18 @@ def test_offsets_past_32_bits(kda):
     got = ro[-9:].cpu()
     ref = host64(tail) + host64(y[-9:])
     assert np.all(np.abs(host64(got) - ref) <= 1.01 * U[BF] * np.abs(ref) + 4 * U32 * np.abs(ref))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("rows", [512, 513])
+@pytest.mark.parametrize("dim", [300, 768, 1000, 2050, 4096])
+def test_wide_rows_many_of_them(kda, dtype, rows, dim):
+    """Up to 512 rows a thread takes one vector of a row, beyond that two."""
+    x, z = draw(31, rows, dim, dtype=dtype), draw(32, rows, dim, dtype=dtype)
+    w, v, r = draw(33, dim), draw(34, dim), draw(35, rows, dim)
+    check_gated(x, w, z, "silu", False, 1e-6, kda.gated_norm(c(x), c(w), c(z), "silu"))
+    ro, y = kda.block_norm(c(x), c(r), c(w), c(v), c(z), "sigmoid", scale=0.5)
+    check_block(x, r, w, v, z, "sigmoid", None, 0.5, 1e-6, ro, y)
+    x[3] = float("nan")  # a row of its own
+    same = kda.gated_norm(c(x), c(w), c(z), "silu")
+    assert torch.isnan(same[3]).all() and torch.isfinite(same[:3]).all() and torch.isfinite(same[4:]).all()
