@@ -435,3 +435,11 @@ def test_prefill_few_tokens_per_sequence(kda, dk, dv, Hk):
     o2, h2 = run(kda, cuda(b))
     assert torch.equal(o2[:40], o[:40]) and torch.equal(o2[64:], o[64:]) and torch.equal(h2[3:], ht[3:])
     assert torch.isinf(o2[40:64, 1, 3]).any() or torch.isnan(o2[40:64, 1, 3]).any()
+
+
+@pytest.mark.parametrize("H,T", [(1, 700), (2, 4097), (3, 2500)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_prefill_joins_of_every_length(kda, H, T, dtype):
+    """Few heads: the join's workgroups are a wave, its segments come in runs of 16, 8, 4, 2, 1."""
+    i = linear_inputs(29, [T], H, H, 64, 64, dtype)
+    check_linear(i, *run(kda, cuda(i)))
