@@ -1,7 +1,8 @@
 // kda_linear.hip -- linear attention with one decay per head over packed
 // sequences (kda_linear_prefill).
 //
-// In chunks of 64 tokens (32 in fp32), with G_i the sum of the log-decays of a chunk's
+// In chunks of 64 tokens (32 in fp32 and for short sequences), with G_i the sum of
+// the log-decays of a chunk's
 // tokens up to and with i, G the whole chunk's and S the state before it:
 //     o_i = scale (exp(G_i) S^T q_i + sum_{j <= i} exp(G_i - G_j) (q_i . k_j) v_j)
 //     S  <- exp(G) S + sum_j exp(G - G_j) k_j v_j^T
