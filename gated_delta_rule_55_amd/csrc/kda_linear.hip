@@ -2,8 +2,8 @@
 // sequences (kda_linear_prefill).
 //
 // In chunks of 64 tokens (32 in fp32 and for short sequences), with G_i the sum of
-// the log-decays of a chunk's
-// tokens up to and with i, G the whole chunk's and S the state before it:
+// the log-decays of a chunk's tokens up to and with i, G the whole chunk's and S
+// the state before it:
 //     o_i = scale (exp(G_i) S^T q_i + sum_{j <= i} exp(G_i - G_j) (q_i . k_j) v_j)
 //     S  <- exp(G) S + sum_j exp(G - G_j) k_j v_j^T
 // Every factor is at most 1 when g <= 0.  The chunks of a sequence follow one
@@ -606,7 +606,7 @@ void linear_kernel(LinearParams P) {
 
 // Pass 2: the state each segment of a split sequence starts from, in place of
 // the segments' own states.  A thread walks X vectors of four elements through
-// the segments, four segments loaded at a time; bound by the workspace's
+// the segments, up to 16 / X segments loaded at a time; bound by the workspace's
 // traffic (32,768 tokens x 32 heads: 12 us), two vectors a thread keeping the
 // workgroups few, or by the walk where there are few of them: one vector then.
 // Workgroups go by sequence or, where there are more sequences than segment

@@ -147,7 +147,7 @@ def linear_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.T
     their first stride may differ from a dense tensor's (a multiple of 16
     bytes).  state_indices (int32 [N] on the device): h0 and ht are pools
     [S, H, dk, dv] (ht defaults to h0: in place), sequence n uses slot
-    state_indices[n], a negative slot skips it.  workspace: a buffer of
+    state_indices[n], a negative slot skips it; no slot twice.  workspace: a buffer of
     linear_workspace_bytes bytes, one for each call that may overlap another
     (a captured graph keeps its own); allocated here when None.
     cu_seqlens is read on the device: contents that break its rules give
@@ -225,7 +225,7 @@ def linear_decode(state: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torc
     q, k: [N, Hk, dk]; v: [N, H, dv]; g: fp32 [N, H] or [H].  Returns o
     [N, H, dv].  state_indices (int32 [N] on the device): `state` is then a
     pool [S, H, dk, dv] and sequence n updates slot state_indices[n]; a
-    negative slot skips it (its o is left as it was).  Strides as in
+    negative slot skips it (its o is left as it was); no slot twice.  Strides as in
     linear_prefill."""
     if _fast is not None and stream is None:
         done = _fast.linear_decode(state, q, k, v, g, scale, out, state_indices)
