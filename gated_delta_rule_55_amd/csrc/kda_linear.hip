@@ -747,7 +747,11 @@ int64_t linear_segment(int64_t t_total, int n_seqs, int n_heads, int dv, bool bf
   // 33,001 tokens in all: 395 us, with eight or sixteen 455 to 460)
   const int64_t waves = 256 * (n_seqs == 1 ? 8 : 12);
   const int64_t want = (t_total * n_heads * (dv / 32) + waves - 1) / waves;
-  const int64_t seg = (want + kGrain - 1) / kGrain * kGrain;
+  int64_t seg = (want + kGrain - 1) / kGrain * kGrain;
+  // segments of one or two chunks leave most of the time to launches, states and
+  // their join: half as many then (2,048 tokens x 32 heads: 51 us -> 48; 4,096,
+  // whose segments have four, 71 -> 73)
+  if (bf16 && seg <= 128) seg = (2 * want + kGrain - 1) / kGrain * kGrain;
   // below that a split costs two launches more: taken for short sequences only
   // when they alone leave CUs idle (512 tokens x 32 heads in bf16: 31 us against
   // 32 in one segment, 1,024: 36 against 59), and not for 256 tokens (26 against

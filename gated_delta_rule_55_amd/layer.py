@@ -119,7 +119,8 @@ def _decay(g, rows, H, dev):
 
 def linear_workspace_bytes(T: int, H: int, dk: int, dv: int, n_seqs: int = 1,
                            dtype: torch.dtype = torch.bfloat16) -> int:
-    """Bytes of workspace linear_prefill needs for these sizes (0: none)."""
+    """Bytes of workspace linear_prefill needs for these sizes (0: none).  Not
+    monotonic in T: a buffer for several sizes takes their maximum."""
     return _al.linear_workspace_bytes(_al.make(
         _al.LinearPrefillDesc, dtype=_DTYPES[dtype], n_seqs=n_seqs, n_heads=H, dk=dk, dv=dv,
         t_total=T))

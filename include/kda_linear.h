@@ -118,7 +118,9 @@ typedef struct {
 
 /* Bytes of device workspace kda_linear_prefill needs for this descriptor
  * (depends on its sizes only; 0 where it needs none).  *status (host, may be
- * NULL) receives the kda_status of the check; 0 is returned when it fails. */
+ * NULL) receives the kda_status of the check; 0 is returned when it fails.
+ * A shorter batch may need more than a longer one (its segments are shorter):
+ * a buffer for several shapes takes the largest of their sizes. */
 size_t kda_linear_workspace_bytes(const kda_linear_prefill_desc* d, int* status);
 
 /* Enqueue the prefill on `stream`.  workspace: device buffer of at least
