@@ -7,13 +7,18 @@
 // point returns, or None for any call it does not take: tensors that are not
 // dense or not on the current device, subclasses, a descriptor that the library
 // refuses, an allocation that fails.  layer.py then makes the call itself, with
-// its own checks and errors.  Nothing is kept between calls.
+// its own checks and errors.  None always means that nothing was enqueued: the
+// results are made ready before the library is called, and a launch that fails
+// raises KdaError, since a second call would update states in place twice.
+// Nothing is kept between calls.
 #include <Python.h>
 #include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/ops/empty.h>
+
+#include <utility>
 
 #include "kda_linear.h"
 #include "kda_norm.h"
@@ -96,20 +101,40 @@ struct Args {
 
 int type_of(at::ScalarType t) { return t == at::kBFloat16 ? KDA_DTYPE_BF16 : KDA_DTYPE_F32; }
 
-PyObject* wrap(PyObject* given, at::Tensor& made) {
-  if (made.defined()) return THPVariable_Wrap(std::move(made));
+// An owned reference, or none.
+struct Ref {
+  PyObject* p = nullptr;
+  Ref() = default;
+  explicit Ref(PyObject* owned) : p(owned) {}
+  Ref(Ref&& o) noexcept : p(o.release()) {}
+  Ref(const Ref&) = delete;
+  Ref& operator=(const Ref&) = delete;
+  ~Ref() { Py_XDECREF(p); }
+  PyObject* release() { return std::exchange(p, nullptr); }
+};
+
+Ref wrap(PyObject* given, at::Tensor& made) {
+  if (made.defined()) return Ref(THPVariable_Wrap(std::move(made)));
   Py_INCREF(given);
-  return given;
+  return Ref(given);
 }
 
-PyObject* pair(PyObject* a, PyObject* b) {
-  PyObject* t = a && b ? PyTuple_Pack(2, a, b) : nullptr;
-  Py_XDECREF(a);
-  Py_XDECREF(b);
-  return t;
+Ref pair(const Ref& a, const Ref& b) { return Ref(a.p && b.p ? PyTuple_Pack(2, a.p, b.p) : nullptr); }
+
+// `result` when the library took the call, None when its checks refused it, and
+// KdaError when a launch failed, after which part of the call may run.
+PyObject* answer(int status, const char* what, Ref& result) {
+  if (status == KDA_OK) return result.release();
+  if (status != KDA_ERR_HIP) Py_RETURN_NONE;
+  const Ref module(PyImport_ImportModule("gated_delta_rule_55_amd._abi"));
+  const Ref type(module.p ? PyObject_GetAttrString(module.p, "KdaError") : nullptr);
+  const Ref error(type.p ? PyObject_CallFunction(type.p, "is", status, what) : nullptr);
+  if (error.p) PyErr_SetObject(type.p, error.p);
+  return nullptr;
 }
 
-// Runs f, with None for everything it throws.
+// Runs f, with None for everything it throws, which is before its call of the
+// library.
 template <typename F>
 PyObject* guarded(F f) {
   try {
@@ -179,8 +204,10 @@ PyObject* linear_decode(PyObject*, PyObject* const* p, Py_ssize_t n) {
     d.v = r.v;
     d.g = static_cast<const float*>(r.g);
     d.n_slots = d.state_indices ? (int32_t)S : 0;
-    if (kda_linear_decode(&d, a.stream()) != KDA_OK) Py_RETURN_NONE;
-    return wrap(p[6], made);
+    Ref result = wrap(p[6], made);
+    if (!result.p) return nullptr;
+    void* const stream = a.stream();
+    return answer(kda_linear_decode(&d, stream), "kda_linear_decode", result);
   });
 }
 
@@ -253,8 +280,10 @@ PyObject* linear_prefill(PyObject*, PyObject* const* p, Py_ssize_t n) {
         ws = made.data_ptr();
       }
     }
-    if (kda_linear_prefill(&d, ws, bytes, a.stream()) != KDA_OK) Py_RETURN_NONE;
-    return pair(wrap(p[7], out), wrap(hto, ht));
+    Ref result = pair(wrap(p[7], out), wrap(hto, ht));
+    if (!result.p) return nullptr;
+    void* const stream = a.stream();
+    return answer(kda_linear_prefill(&d, ws, bytes, stream), "kda_linear_prefill", result);
   });
 }
 
@@ -289,8 +318,10 @@ PyObject* gated_norm(PyObject*, PyObject* const* p, Py_ssize_t n) {
     d.dim = (int32_t)dim;
     d.rows = rows;
     d.x = x->data_ptr();
-    if (kda_gated_norm(&d, a.stream()) != KDA_OK) Py_RETURN_NONE;
-    return wrap(p[6], made);
+    Ref result = wrap(p[6], made);
+    if (!result.p) return nullptr;
+    void* const stream = a.stream();
+    return answer(kda_gated_norm(&d, stream), "kda_gated_norm", result);
   });
 }
 
@@ -325,8 +356,10 @@ PyObject* block_norm(PyObject*, PyObject* const* p, Py_ssize_t n) {
     d.dim = (int32_t)dim;
     d.rows = rows;
     d.x = x->data_ptr();
-    if (kda_block_norm(&d, a.stream()) != KDA_OK) Py_RETURN_NONE;
-    return pair(wrap(p[9], rout), wrap(p[10], out));
+    Ref result = pair(wrap(p[9], rout), wrap(p[10], out));
+    if (!result.p) return nullptr;
+    void* const stream = a.stream();
+    return answer(kda_block_norm(&d, stream), "kda_block_norm", result);
   });
 }
 

@@ -1,0 +1,97 @@
+"""What the module _fast does with the library's answers, without a GPU: built
+from its own source for CPU tensors and with stand-ins for the library's entry
+points (native_on_host.cpp)."""
+import ctypes
+import importlib.machinery
+import importlib.util
+import os
+import shutil
+import subprocess
+import sysconfig
+
+import pytest
+import torch
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+pytestmark = pytest.mark.skipif(
+    not (shutil.which("g++") and os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h"))),
+    reason="needs g++ and Python's headers")
+
+
+@pytest.fixture(scope="module")
+def fast(tmp_path_factory):
+    from gated_delta_rule_55_amd import _abi, build
+
+    if not os.path.exists(_abi.LIB_PATH):
+        pytest.skip("libkda.so not built")  # KdaError asks it for its texts
+    out = str(tmp_path_factory.mktemp("native") / "_fast.so")
+    flags = build._fast_command()
+    head = [f for f in flags if f.startswith(("-I", "-isystem", "-D", "-std"))]
+    libs = [f for f in flags if f.startswith(("-L", "-l")) and "libkda" not in f]
+    subprocess.run(["g++", "-O1", "-fPIC", "-shared", "-Wl,-Bsymbolic", *head, f"-I{build.CSRC}",
+                    os.path.join(ROOT, "tests", "native_on_host.cpp"), "-o", out, *libs], check=True)
+    loader = importlib.machinery.ExtensionFileLoader("_fast", out)
+    m = importlib.util.module_from_spec(importlib.util.spec_from_loader("_fast", loader))
+    loader.exec_module(m)
+    m.host = ctypes.CDLL(out)
+    return m
+
+
+def calls():
+    """One call of each entry point that makes its outputs, and one that is given them."""
+    q, v, g = torch.zeros(3, 2, 32), torch.zeros(3, 4, 32), torch.zeros(3, 4)
+    st, x, w = torch.zeros(3, 4, 32, 32), torch.zeros(5, 64), torch.ones(64)
+    cu = torch.tensor([0, 1, 2, 3], dtype=torch.int32)
+    yield "linear_decode", (st, q, q.clone(), v, g, None, None, None)
+    yield "linear_decode", (st, q, q.clone(), v, g, None, torch.zeros_like(v), None)
+    yield "linear_prefill", (q, q.clone(), v, g, st, cu, None, None, None, None, True, None, False)
+    yield "linear_prefill", (q, q.clone(), v, g, st, cu, None, torch.zeros_like(v), st, None, True, None, False)
+    yield "gated_norm", (x, w, None, None, False, 1e-6, None)
+    yield "gated_norm", (x, w, None, None, False, 1e-6, x)
+    yield "block_norm", (x, x.clone(), w, w, None, None, None, 1.0, 1e-6, None, None)
+    yield "block_norm", (x, w.expand(5, 64).contiguous(), w, w, None, None, None, 1.0, 1e-6, x.clone(), x)
+
+
+CALLS = list(calls())
+
+
+@pytest.mark.parametrize("name,args", CALLS, ids=[f"{n}-{i % 2}" for i, (n, _) in enumerate(CALLS)])
+def test_a_launch_that_failed_is_not_made_again(fast, name, args):
+    """KDA_ERR_HIP comes after a launch was asked for: a second call could apply
+    the step twice.  It is an error, where every other status hands the call
+    back (None) with nothing enqueued."""
+    from gated_delta_rule_55_amd import KdaError
+
+    def run(status):
+        fast.host.host_reset(status)
+        try:
+            return getattr(fast, name)(*args)
+        finally:
+            assert fast.host.host_calls() == 1
+
+    assert run(0) is not None
+    for refusal in (-1, -2, -3, -4, -5, -6, -8, -9):
+        assert run(refusal) is None
+    with pytest.raises(KdaError) as e:
+        run(-7)
+    assert e.value.status == -7 and "kda_" + name in str(e.value)
+
+
+def test_the_wrapper_passes_the_error_on(fast, monkeypatch):
+    """layer.py makes no call of its own after it."""
+    from gated_delta_rule_55_amd import KdaError, layer
+
+    monkeypatch.setattr(layer, "_fast", fast)
+    monkeypatch.setattr(layer._al, "lib", lambda: pytest.fail("called again"))
+    for name, a in CALLS:
+        fast.host.host_reset(-7)
+        with pytest.raises(KdaError):
+            if name == "linear_prefill":
+                layer.linear_prefill(*a[:6], out=a[7], ht=a[8])
+            elif name == "linear_decode":
+                layer.linear_decode(*a[:5], out=a[6])
+            elif name == "gated_norm":
+                layer.gated_norm(a[0], a[1], out=a[6])
+            else:
+                layer.block_norm(a[0], a[1], a[2], a[3], residual_out=a[9], out=a[10])
+        assert fast.host.host_calls() == 1
