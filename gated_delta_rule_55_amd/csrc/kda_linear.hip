@@ -36,6 +36,7 @@
 // half a gigabyte in the 256 MB cache.
 #include <type_traits>
 
+#include "kda_enqueue.h"
 #include "kda_linear_launch.h"
 #include "kda_linear_ops.h"
 
@@ -682,8 +683,7 @@ hipError_t launch(const LinearParams& p, bool split, hipStream_t stream) {
   const int64_t blocks = placed_blocks(linear_segments(p.T, p.N, p.L), p.H / HG, p.rep / HG);
   constexpr int VW = DV * HG;
   if (split) {
-    linear_kernel<T, kChunk<T>, DK, VW, HG, false><<<(unsigned)blocks, 2 * VW, 0, stream>>>(p);
-    hipError_t e = hipGetLastError();
+    hipError_t e = enqueue(linear_kernel<T, kChunk<T>, DK, VW, HG, false>, (unsigned)blocks, 2 * VW, stream, p);
     if (e != hipSuccess) return e;
     constexpr int parts = DK * DV / 1024, parts2 = (parts + 1) / 2;
     const bool marks = p.T / p.L < p.N;
@@ -691,12 +691,11 @@ hipError_t launch(const LinearParams& p, bool split, hipStream_t stream) {
     // workgroups of a wave where those of four would leave CUs without one (63
     // segments of 16 heads of 64 x 64: 9.5 us against 11.6)
     if (most * parts <= 128)
-      linear_join_kernel<1><<<(unsigned)(most * parts * 4), 64, 0, stream>>>(p, DK * DV, parts * 4, marks);
+      e = enqueue(linear_join_kernel<1>, (unsigned)(most * parts * 4), 64, stream, p, DK * DV, parts * 4, marks);
     else if (most * parts <= 512)
-      linear_join_kernel<1><<<(unsigned)(most * parts), 256, 0, stream>>>(p, DK * DV, parts, marks);
+      e = enqueue(linear_join_kernel<1>, (unsigned)(most * parts), 256, stream, p, DK * DV, parts, marks);
     else
-      linear_join_kernel<2><<<(unsigned)(most * parts2), 256, 0, stream>>>(p, DK * DV, parts2, marks);
-    e = hipGetLastError();
+      e = enqueue(linear_join_kernel<2>, (unsigned)(most * parts2), 256, stream, p, DK * DV, parts2, marks);
     if (e != hipSuccess) return e;
   }
   // Sequences of few tokens in bf16 are mostly loads and stores of states: chunks
@@ -704,13 +703,10 @@ hipError_t launch(const LinearParams& p, bool split, hipStream_t stream) {
   // 32 heads of 128: 20 us against 24).  Longer ones lose a little by it (64 x
   // 1,024 tokens: 267 us against 256).
   if constexpr (sizeof(T) == 2) {
-    if (!split && p.T <= 64 * (int64_t)p.N) {
-      linear_kernel<T, 32, DK, VW, HG, true><<<(unsigned)blocks, 2 * VW, 0, stream>>>(p);
-      return hipGetLastError();
-    }
+    if (!split && p.T <= 64 * (int64_t)p.N)
+      return enqueue(linear_kernel<T, 32, DK, VW, HG, true>, (unsigned)blocks, 2 * VW, stream, p);
   }
-  linear_kernel<T, kChunk<T>, DK, VW, HG, true><<<(unsigned)blocks, 2 * VW, 0, stream>>>(p);
-  return hipGetLastError();
+  return enqueue(linear_kernel<T, kChunk<T>, DK, VW, HG, true>, (unsigned)blocks, 2 * VW, stream, p);
 }
 
 // Heads narrower than 128 that share a key head are taken together, four waves

@@ -15,6 +15,7 @@
 // CB is the whole row of DV columns, or 32 of them where there are fewer than
 // 512 (sequence, head) pairs: one sequence of 32 heads is 128 workgroups
 // then, and the 3.5 us that its launch takes anyway.
+#include "kda_enqueue.h"
 #include "kda_linear_launch.h"
 #include "kda_linear_ops.h"
 
@@ -90,12 +91,9 @@ __global__ __launch_bounds__(256) void linear_decode_kernel(DecodeParams P) {
 template <typename T, typename TS, int DK, int DV>
 hipError_t launch(const LinearDecodeArgs& a, const DecodeParams& p, hipStream_t stream) {
   const int64_t nh = (int64_t)a.n_seqs * a.n_heads;
-  if (DV > 32 && nh < 512) {
-    linear_decode_kernel<T, TS, DK, DV, 32><<<(unsigned)(nh * (DV / 32)), 256, 0, stream>>>(p);
-  } else {
-    linear_decode_kernel<T, TS, DK, DV, DV><<<(unsigned)nh, 256, 0, stream>>>(p);
-  }
-  return hipGetLastError();
+  if (DV > 32 && nh < 512)
+    return enqueue(linear_decode_kernel<T, TS, DK, DV, 32>, (unsigned)(nh * (DV / 32)), 256, stream, p);
+  return enqueue(linear_decode_kernel<T, TS, DK, DV, DV>, (unsigned)nh, 256, stream, p);
 }
 
 template <typename T, typename TS>

@@ -15,6 +15,7 @@
 // around a block with every option, 1.34 GB, 249 us (5.4 TB/s).  Rows of 4,097,
 // whose vectors are not aligned, run at 4.1 to 4.9 TB/s.
 #include "kda_device.h"
+#include "kda_enqueue.h"
 #include "kda_norm_launch.h"
 
 namespace kda {
@@ -269,8 +270,7 @@ struct GatedLaunch {
   hipStream_t stream;
   template <int TPR, int NI>
   hipError_t run() const {
-    gated_norm_kernel<T, TPR, NI><<<grid_of<TPR>(a.rows), threads_of<TPR>(), 0, stream>>>(a);
-    return hipGetLastError();
+    return enqueue(gated_norm_kernel<T, TPR, NI>, grid_of<TPR>(a.rows), threads_of<TPR>(), stream, a);
   }
 };
 
@@ -280,8 +280,7 @@ struct BlockLaunch {
   hipStream_t stream;
   template <int TPR, int NI>
   hipError_t run() const {
-    block_norm_kernel<T, TR, TPR, NI><<<grid_of<TPR>(a.rows), threads_of<TPR>(), 0, stream>>>(a);
-    return hipGetLastError();
+    return enqueue(block_norm_kernel<T, TR, TPR, NI>, grid_of<TPR>(a.rows), threads_of<TPR>(), stream, a);
   }
 };
 

@@ -1,0 +1,109 @@
+"""The launches of linear attention and the norms without a GPU: the library
+over stand-ins for the HIP runtime's launch calls (fake_hip.cpp), in a child
+process that preloads them.  Which kernels a descriptor enqueues, and what
+becomes of a launch's status."""
+import os
+import shutil
+import subprocess
+import sys
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+pytestmark = pytest.mark.skipif(
+    not (shutil.which("g++") and os.path.exists(os.path.join(ROOT, "gated_delta_rule_55_amd", "libkda.so"))),
+    reason="needs g++ and libkda.so")
+
+CHILD = """
+import ctypes, sys
+sys.path[:0] = [{root!r}]
+from gated_delta_rule_55_amd import _abi, _abi_layer as al
+fake = ctypes.CDLL({fake!r})
+fake.fake_log.restype = ctypes.c_char_p
+L = al.lib()
+
+def prefill_desc(**over):
+    kw = dict(dtype=2, n_seqs=1, n_heads=32, dk=128, dv=128, t_total=300, q=1 << 40, k=2 << 40, v=3 << 40,
+              g=4 << 40, o=5 << 40, h0=6 << 40, ht=6 << 40, cu_seqlens=7 << 40)
+    kw.update(over)
+    return al.make(al.LinearPrefillDesc, **kw)
+
+def prefill(**over):
+    d = prefill_desc(**over)
+    return L.kda_linear_prefill(ctypes.byref(d), 8 << 40, 1 << 40, None)
+
+def decode(**over):
+    kw = dict(dtype=2, n_seqs=3, n_heads=4, dk=64, dv=128, state=6 << 40, q=1 << 40, k=2 << 40, v=3 << 40,
+              g=4 << 40, o=5 << 40)
+    kw.update(over)
+    d = al.make(al.LinearDecodeDesc, **kw)
+    return L.kda_linear_decode(ctypes.byref(d), None)
+
+def gated(**over):
+    kw = dict(dtype=2, dim=128, rows=9, x=1 << 40, y=1 << 40)
+    kw.update(over)
+    d = al.make(al.GatedNormDesc, **kw)
+    return L.kda_gated_norm(ctypes.byref(d), None)
+
+def block(**over):
+    kw = dict(dtype=2, dim=4096, rows=9, scale=1.0, x=1 << 40, r=2 << 40, r_out=2 << 40)
+    kw.update(over)
+    d = al.make(al.BlockNormDesc, **kw)
+    return L.kda_block_norm(ctypes.byref(d), None)
+
+def kernels():
+    return [ln.split()[0] for ln in fake.fake_log().decode().splitlines()]
+
+def reset(older=0, status=0, fails_from=1 << 30):
+    fake.fake_reset(older, status, fails_from)
+
+def needs(**over):
+    return L.kda_linear_workspace_bytes(ctypes.byref(prefill_desc(**over)), None)
+
+# a prefill that splits sequences needs a workspace, and three launches
+CALLS = [(prefill, over, 3 if needs(**over) else 1) for over in (
+             dict(), dict(t_total=32768), dict(dtype=1, t_total=5000), dict(n_seqs=24), dict(t_total=64))]
+assert sorted(n for _, _, n in CALLS) == [1, 1, 3, 3, 3]
+CALLS += [(decode, dict(), 1), (decode, dict(n_seqs=500), 1), (gated, dict(), 1), (gated, dict(dtype=1, dim=1000), 1),
+          (block, dict(), 1)]
+"""
+
+
+@pytest.fixture(scope="module")
+def child(tmp_path_factory):
+    tmp = tmp_path_factory.mktemp("fake_hip")
+    fake = str(tmp / "libfake_hip.so")
+    subprocess.run(["g++", "-std=c++17", "-O1", "-fPIC", "-shared", os.path.join(ROOT, "tests", "fake_hip.cpp"),
+                    "-o", fake], check=True)
+
+    def run(body):
+        script = tmp / "child.py"
+        script.write_text(CHILD.format(root=ROOT, fake=fake) + body + "\nprint('child ok')\n")
+        preload = " ".join(x for x in (fake, os.environ.get("LD_PRELOAD")) if x)
+        p = subprocess.run([sys.executable, str(script)], env=dict(os.environ, LD_PRELOAD=preload),
+                           capture_output=True, text=True, timeout=120)
+        assert p.returncode == 0 and "child ok" in p.stdout, p.stdout + p.stderr
+
+    return run
+
+
+def test_an_older_error_is_not_a_launch_s_own(child):
+    """An error that an earlier HIP call of the thread left neither fails a good
+    launch nor is taken from whoever looks for it."""
+    child("""
+for call, over, n in CALLS:
+    reset(older=101)
+    assert call(**over) == 0, (call.__name__, over)
+    assert len(kernels()) == n and fake.fake_older() == 101, (call.__name__, over, kernels())
+""")
+
+
+def test_a_launch_that_fails_ends_the_call(child):
+    """Its error is the call's, no launch follows it, and none is left behind."""
+    child("""
+for call, over, n in CALLS:
+    for at in range(n):
+        reset(status=719, fails_from=at)
+        assert call(**over) == -7 and L.kda_last_hip_error() == 719, (call.__name__, over)
+        assert len(kernels()) == at + 1 and fake.fake_older() == 0, (call.__name__, over, kernels())
+""")
