@@ -25,6 +25,15 @@
 
 namespace {
 
+// Lets other Python threads run: around allocations and the library's calls,
+// both of which may wait for the device.
+struct NoGil {
+  PyThreadState* state = PyEval_SaveThread();
+  NoGil() = default;
+  NoGil(const NoGil&) = delete;
+  ~NoGil() { PyEval_RestoreThread(state); }
+};
+
 // A dense tensor argument of one device and type; `ok` turns false at the first
 // argument that is none.
 struct Args {
@@ -87,6 +96,7 @@ struct Args {
     return 0;
   }
   at::Tensor empty(at::IntArrayRef shape, at::ScalarType type) const {
+    const NoGil no_gil;
     return at::empty(shape, at::TensorOptions().dtype(type).device(at::Device(at::kCUDA, dev)));
   }
   // `o`'s tensor, or a new one where it is None; `made` then holds it.
@@ -131,6 +141,12 @@ PyObject* answer(int status, const char* what, Ref& result) {
   const Ref error(type.p ? PyObject_CallFunction(type.p, "is", status, what) : nullptr);
   if (error.p) PyErr_SetObject(type.p, error.p);
   return nullptr;
+}
+
+template <typename F>
+int unlocked(F call) {
+  const NoGil no_gil;
+  return call();
 }
 
 // Runs f, with None for everything it throws, which is before its call of the
@@ -207,7 +223,7 @@ PyObject* linear_decode(PyObject*, PyObject* const* p, Py_ssize_t n) {
     Ref result = wrap(p[6], made);
     if (!result.p) return nullptr;
     void* const stream = a.stream();
-    return answer(kda_linear_decode(&d, stream), "kda_linear_decode", result);
+    return answer(unlocked([&] { return kda_linear_decode(&d, stream); }), "kda_linear_decode", result);
   });
 }
 
@@ -283,7 +299,7 @@ PyObject* linear_prefill(PyObject*, PyObject* const* p, Py_ssize_t n) {
     Ref result = pair(wrap(p[7], out), wrap(hto, ht));
     if (!result.p) return nullptr;
     void* const stream = a.stream();
-    return answer(kda_linear_prefill(&d, ws, bytes, stream), "kda_linear_prefill", result);
+    return answer(unlocked([&] { return kda_linear_prefill(&d, ws, bytes, stream); }), "kda_linear_prefill", result);
   });
 }
 
@@ -321,7 +337,7 @@ PyObject* gated_norm(PyObject*, PyObject* const* p, Py_ssize_t n) {
     Ref result = wrap(p[6], made);
     if (!result.p) return nullptr;
     void* const stream = a.stream();
-    return answer(kda_gated_norm(&d, stream), "kda_gated_norm", result);
+    return answer(unlocked([&] { return kda_gated_norm(&d, stream); }), "kda_gated_norm", result);
   });
 }
 
@@ -359,7 +375,7 @@ PyObject* block_norm(PyObject*, PyObject* const* p, Py_ssize_t n) {
     Ref result = pair(wrap(p[9], rout), wrap(p[10], out));
     if (!result.p) return nullptr;
     void* const stream = a.stream();
-    return answer(kda_block_norm(&d, stream), "kda_block_norm", result);
+    return answer(unlocked([&] { return kda_block_norm(&d, stream); }), "kda_block_norm", result);
   });
 }
 

@@ -95,3 +95,13 @@ def test_the_wrapper_passes_the_error_on(fast, monkeypatch):
             else:
                 layer.block_norm(a[0], a[1], a[2], a[3], residual_out=a[9], out=a[10])
         assert fast.host.host_calls() == 1
+
+
+def test_the_library_is_called_without_the_interpreter_lock(fast):
+    """A launch may wait for room in its queue: other threads go on meanwhile
+    (one of them may run the host function that the queue waits for)."""
+    for status in (0, -2):
+        for name, args in CALLS:
+            fast.host.host_reset(status)
+            getattr(fast, name)(*args)
+            assert fast.host.host_calls() == 1 and fast.host.host_calls_with_gil() == 0
