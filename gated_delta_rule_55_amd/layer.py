@@ -46,6 +46,8 @@ _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device
 def _on(dev, stream):
     """A context in which `dev` is current and `stream` (or the device's current
     stream) is the stream that torch allocates for."""
+    if stream is not None and stream.device != dev:
+        raise ValueError(f"stream is on {stream.device}, expected {dev}")
     if stream is None and dev.index == _current_device():
         return _HERE
     return _guard(dev, stream)
