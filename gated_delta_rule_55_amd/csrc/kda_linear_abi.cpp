@@ -71,8 +71,10 @@ int check_linear(const kda_linear_prefill_desc* d, kda::LinearPrefillArgs* a) {
   a->dv = d->dv;
   a->t_total = d->t_total;
   a->scale = d->scale != 0.f ? d->scale : 1.0f / std::sqrt((float)d->dk);
-  // workgroups: segments x heads, and 8 per segment length and head that join them
+  // the kernels hold a segment's length in 32 bits
   const int64_t seg = kda::linear_segment(a->t_total, a->n_seqs, a->n_heads, a->dv, a->bf16);
+  if (seg > INT32_MAX) return KDA_ERR_SHAPE;
+  // workgroups: segments x heads, and 8 per segment length and head that join them
   if ((kda::linear_segments(a->t_total, a->n_seqs, seg) + 8) * H >= kMaxBlocks ||
       a->t_total / seg * H * 8 >= kMaxBlocks)
     return KDA_ERR_SHAPE;

@@ -70,7 +70,8 @@ typedef struct {
   int32_t n_k_heads;            /* Hk, dividing H; 0 = H                        */
   int32_t dk, dv;               /* each in {32, 64, 128}                        */
   int32_t decay;                /* kda_decay                                    */
-  int64_t t_total;              /* packed tokens, 0 .. 2^31 - 65                */
+  int64_t t_total;              /* packed tokens, 0 .. 2^31 - 65; v holds fewer */
+                                /* than 2^47 values                             */
   float scale;                  /* 0 = dk^-1/2                                  */
   int32_t state_dtype;          /* kda_dtype of h0 and ht; 0 = fp32; bf16 with  */
                                 /* bf16 inputs only                             */

@@ -107,3 +107,23 @@ for call, over, n in CALLS:
         assert call(**over) == -7 and L.kda_last_hip_error() == 719, (call.__name__, over)
         assert len(kernels()) == at + 1 and fake.fake_older() == 0, (call.__name__, over, kernels())
 """)
+
+
+def test_a_segment_past_32_bits_is_refused(child):
+    """Segments grow with tokens x heads x dv; where their length leaves 32 bits
+    the call is refused (such tensors fit no memory), not divided by zero."""
+    child("""
+p = [x << 54 for x in range(1, 6)]
+big = dict(zip("qkvgo", p), t_total=1 << 30, n_heads=2048, n_k_heads=1, dk=32, h0=None, ht=None, cu_seqlens=None)
+for over, want in ((dict(), -2), (dict(n_heads=4096, dv=64), -2), (dict(t_total=1 << 31), -2),
+                   (dict(t_total=(1 << 31) - 65, n_heads=65535, n_k_heads=1, dv=32), -2),
+                   (dict(n_heads=1024), -2),  # tokens x heads x dv / 32 / 2,048 = 2^31
+                   (dict(n_heads=1024, t_total=(1 << 30) - 64), 0), (dict(n_heads=512), 0)):
+    kw = dict(big, **over)
+    st = ctypes.c_int(9)
+    reset()
+    L.kda_linear_workspace_bytes(ctypes.byref(prefill_desc(**kw)), ctypes.byref(st))
+    assert st.value == want, over
+    assert prefill(**kw) == want, over
+    assert (len(kernels()) > 0) == (want == 0), over
+""")
