@@ -127,3 +127,32 @@ for over, want in ((dict(), -2), (dict(n_heads=4096, dv=64), -2), (dict(t_total=
     assert prefill(**kw) == want, over
     assert (len(kernels()) > 0) == (want == 0), over
 """)
+
+
+def test_which_prefill_kernels_the_gpu_tests_reach(child):
+    """The sizes of test_gpu_linear_kernels.py enqueue what they are named after,
+    and together every instance that a call can reach."""
+    child("""
+import re
+sys.path[:0] = [{tests!r}]
+import linear_kernel_cases as lk
+seen = set()
+for dtype, kind in lk.KINDS:
+    for dk, dv, H, Hk in lk.DIMS:
+        lengths = lk.lengths_of(dtype, kind, H)
+        reset()
+        assert prefill(dtype=2 if dtype == "bf16" else 1, n_seqs=len(lengths), t_total=sum(lengths), n_heads=H,
+                       n_k_heads=Hk, dk=dk, dv=dv) == 0
+        hg = lk.heads_a_workgroup(dv, H, Hk)
+        got = [re.findall(r"linear_kernelI(?:DF16b|u6__bf16|f)Li(\\d+)ELi(\\d+)ELi(\\d+)ELi(\\d+)ELb([01])E", k)
+               for k in kernels()]
+        got = [tuple(int(x) for x in m[0]) for m in got if m]
+        chunk = 64 if dtype == "bf16" and kind != "few" else 32
+        want = [(chunk, dk, dv * hg, hg, 1)]
+        if kind == "split":
+            want = [(chunk, dk, dv * hg, hg, 0)] + want
+        assert got == want, (dtype, kind, dk, dv, H, Hk, kernels())
+        seen |= {{(dtype,) + w for w in want}}
+# bf16: outputs in both chunk lengths and the segment pass; fp32: outputs and the segment pass
+assert len(seen) == 15 * 3 + 15 * 2, len(seen)
+""".format(tests=os.path.join(ROOT, "tests")))
