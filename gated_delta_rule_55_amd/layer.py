@@ -154,7 +154,8 @@ def linear_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.T
     linear_workspace_bytes bytes, one for each call that may overlap another
     (a captured graph keeps its own); allocated here when None.
     cu_seqlens is read on the device: contents that break its rules give
-    unspecified results but no access out of bounds."""
+    unspecified results but no access out of bounds.  A sequence's bits do not
+    depend on what it is packed with, but they may on T and N."""
     if _fast is not None and stream is None and (
             state_dtype is None or (h0 is None and ht is None and state_dtype in _DTYPES)):
         done = _fast.linear_prefill(q, k, v, g, h0, cu_seqlens, scale, out, ht, workspace,

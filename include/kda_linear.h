@@ -32,10 +32,18 @@
  * with are rounded to bf16 (relative 2^-8 at most) on the way to o, while the
  * carried state is updated from products that keep fp32 precision.
  * A log-decay below -200 acts as -200 (exp(-200) is 0 in fp32), so -inf is
- * allowed and forgets the state; NaN propagates.  g > 0 is computed as
- * written.  A value of q, k, v or g that is not finite reaches the outputs of
- * its own and later tokens of its sequence and head, never earlier ones or
- * another sequence's.
+ * allowed and forgets the state; NaN propagates.  g > 0 is allowed, but the
+ * prefill forms the growth over whole chunks and segments: where that leaves
+ * fp32 (past e^88) its results are not finite, also where the state that it
+ * multiplies is zero.  A value of q, k, v or g that is not finite reaches the
+ * outputs of its own and later tokens of its sequence and head, never earlier
+ * ones or another sequence's; an infinite value may arrive there, and in the
+ * state, as NaN.
+ *
+ * A sequence's results depend, bit for bit, on its own data and on the sizes,
+ * types and options of the call, which choose the lengths of chunks and
+ * segments: not on the sequences packed beside it or on its place among them.
+ * In a call of another t_total or N it may be rounded differently.
  */
 #ifndef KDA_LINEAR_H
 #define KDA_LINEAR_H

@@ -88,3 +88,46 @@ def test_short_sequences_of_a_full_batch(kda, dk, dv, H, Hk):
     check_linear(i, o[rows], ht[live], ref=(ro[rows], rh[live], ao[rows], ah[live]))
     for n in (3, N - 2):
         assert torch.all(out[cu[n]:cu[n + 1]] == 4.0) and torch.equal(ht[n].cpu(), i["h0"][n])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("lengths", [[700, 40, 0, 333, 51, 64], [9, 33, 64, 0, 50, 40], [30] * 3 + [45] * 40 + [0, 400] * 12])
+def test_order_of_the_batch_changes_no_bits(kda, dtype, lengths):
+    """Sequences in another order, and beside other sequences of the same number
+    and total length: the same bits, in every chunk length and split or not."""
+    i = linear_inputs(74, lengths, 4, 2, 64, 64, DT[dtype], g_scale=0.1)
+    d = cuda(i)
+    o, ht = kda.linear_prefill(d["q"], d["k"], d["v"], d["g"], d["h0"], d["cu"])
+    cu = i["cu"].numpy()
+    rng = np.random.default_rng(75)
+    for order in (np.arange(len(lengths))[::-1], rng.permutation(len(lengths))):
+        rows = torch.from_numpy(np.concatenate([np.arange(cu[n], cu[n + 1]) for n in order])).cuda()
+        at = torch.from_numpy(order.copy()).cuda()
+        cu2 = torch.tensor([0] + [lengths[n] for n in order]).cumsum(0).to(torch.int32).cuda()
+        o2, ht2 = kda.linear_prefill(*(d[x][rows].contiguous() for x in "qkvg"), d["h0"][at].contiguous(), cu2)
+        assert torch.equal(o2, o[rows]) and torch.equal(ht2, ht[at])
+    # one sequence kept, the others replaced and cut differently
+    n = int(np.argmax(lengths))
+    other = linear_inputs(76, lengths, 4, 2, 64, 64, DT[dtype], g_scale=0.1)
+    rest = [x for x in lengths]
+    del rest[n]
+    total, cuts = sum(rest), np.sort(rng.integers(0, sum(rest) + 1, size=len(rest) - 1))
+    cut = np.diff(np.concatenate([[0], cuts, [total]]))
+    new = [int(x) for x in cut[:2]] + [lengths[n]] + [int(x) for x in cut[2:]]
+    begin = int(sum(new[:2]))
+    m = cuda(other)
+    for x in "qkvg":
+        m[x][begin:begin + lengths[n]] = d[x][cu[n]:cu[n + 1]]
+    m["h0"][2] = d["h0"][n]
+    cu2 = torch.tensor([0] + new).cumsum(0).to(torch.int32).cuda()
+    o2, ht2 = kda.linear_prefill(m["q"], m["k"], m["v"], m["g"], m["h0"], cu2)
+    assert torch.equal(o2[begin:begin + lengths[n]], o[cu[n]:cu[n + 1]]) and torch.equal(ht2[2], ht[n])
+
+
+@pytest.mark.parametrize("beside", [[], [500], [64] * 30])
+def test_a_sequence_alone_and_in_larger_batches(kda, beside):
+    """33 to 64 tokens: in chunks of 32 or 64, within the bounds either way."""
+    for n in (33, 50, 64):
+        i = linear_inputs(77, [n] + beside, 2, 2, 64, 64, DT["bf16"])
+        d = cuda(i)
+        check_linear(i, *kda.linear_prefill(d["q"], d["k"], d["v"], d["g"], d["h0"], d["cu"]))
