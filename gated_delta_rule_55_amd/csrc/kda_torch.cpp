@@ -77,6 +77,13 @@ struct Args {
     }
     return (float)x;
   }
+  // A scale: 0, the default's value, where there is none and for 0 alone.
+  float scale(PyObject* o) {
+    if (o == Py_None) return 0.f;
+    const float x = number(o);
+    if (x == 0.f && flag(o)) ok = false;
+    return x;
+  }
   bool flag(PyObject* o) {
     const int x = PyObject_IsTrue(o);
     if (x < 0) {
@@ -202,7 +209,7 @@ PyObject* linear_decode(PyObject*, PyObject* const* p, Py_ssize_t n) {
     if (S > INT32_MAX) Py_RETURN_NONE;
     d.state = a.ptr(p[0], st->scalar_type(), {S, r.H, r.dk, r.dv});
     d.state_indices = static_cast<const int32_t*>(a.maybe(p[7], at::kInt, {r.R}));
-    d.scale = p[5] == Py_None ? 0.f : a.number(p[5]);
+    d.scale = a.scale(p[5]);
     at::Tensor made;
     d.o = a.output(p[6], a.dt, {r.R, r.H, r.dv}, made);
     if (!a.ok) Py_RETURN_NONE;
@@ -258,7 +265,7 @@ PyObject* linear_prefill(PyObject*, PyObject* const* p, Py_ssize_t n) {
     const int64_t shape[4] = {S, r.H, r.dk, r.dv};
     d.state_indices = static_cast<const int32_t*>(a.maybe(p[11], at::kInt, {N}));
     d.h0 = a.maybe(p[4], sd, shape);
-    d.scale = p[6] == Py_None ? 0.f : a.number(p[6]);
+    d.scale = a.scale(p[6]);
     at::Tensor out, ht;
     d.o = a.output(p[7], a.dt, {r.R, r.H, r.dv}, out);
     PyObject* hto = p[8] == Py_None && keep && p[11] != Py_None ? p[4] : p[8];

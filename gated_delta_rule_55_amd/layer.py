@@ -119,6 +119,16 @@ def _decay(g, rows, H, dev):
     return _al.KDA_DECAY_TOKEN, _dense(g, "g", (rows, H), torch.float32, dev)
 
 
+def _scale(scale) -> float:
+    """A scale as a descriptor holds it: 0 for the default."""
+    if scale is None:
+        return 0.0
+    scale = float(scale)
+    if scale != 0 and abs(scale) <= 2.0 ** -150:
+        raise ValueError(f"scale {scale} is 0 in fp32, which stands for dk^-1/2")
+    return scale
+
+
 def linear_workspace_bytes(T: int, H: int, dk: int, dv: int, n_seqs: int = 1,
                            dtype: torch.dtype = torch.bfloat16) -> int:
     """Bytes of workspace linear_prefill needs for these sizes (0: none).  Not
@@ -203,7 +213,7 @@ def linear_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.T
         htp = None if ht is None else _dense(ht, "ht", shape, sd, dev)
         desc = _al.LinearPrefillDesc(
             ctypes.sizeof(_al.LinearPrefillDesc), _DTYPES[dt], N, H, Hk, dk, dv, decay, T,
-            0.0 if scale is None else scale, _DTYPES[sd], qp, kp, vp, gp, op, qs, ks, vs, os_,
+            _scale(scale), _DTYPES[sd], qp, kp, vp, gp, op, qs, ks, vs, os_,
             h0p, htp, cup, idxp, S)
         L = _al.lib()
         if workspace is None:
@@ -259,7 +269,7 @@ def linear_decode(state: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torc
             op, os_ = _rows3(out, "out", (N, H, dv), dt, dev)
         desc = _al.LINEAR_DECODE.pack(
             _al.LINEAR_DECODE.size, _DTYPES[dt], N, H, Hk, dk, dv, decay,
-            0.0 if scale is None else scale, _DTYPES[state.dtype], sp, qp, kp, vp, gp, op,
+            _scale(scale), _DTYPES[state.dtype], sp, qp, kp, vp, gp, op,
             qs, ks, vs, os_, idxp or 0, S if idxp is not None else 0)
         st = _al.lib().kda_linear_decode(desc, _raw_stream(dev))
     if st != _abi.KDA_OK:

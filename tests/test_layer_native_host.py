@@ -105,3 +105,26 @@ def test_the_library_is_called_without_the_interpreter_lock(fast):
             fast.host.host_reset(status)
             getattr(fast, name)(*args)
             assert fast.host.host_calls() == 1 and fast.host.host_calls_with_gil() == 0
+
+
+@pytest.mark.parametrize("scale", [1e-50, -1e-60, 5e-324])
+def test_a_scale_that_fp32_has_as_zero_is_refused(fast, scale):
+    """0 stands for dk^-1/2: such a scale would give outputs 10^40 times too large."""
+    from gated_delta_rule_55_amd import layer
+
+    fast.host.host_reset(0)
+    for name, a in CALLS[:4]:
+        at = 5 if name == "linear_decode" else 6
+        assert getattr(fast, name)(*a[:at], scale, *a[at + 1:]) is None and fast.host.host_calls() == 0
+    with pytest.raises(ValueError, match="scale"):
+        layer._scale(scale)
+
+
+def test_scales(fast):
+    from gated_delta_rule_55_amd import layer
+
+    assert [layer._scale(x) for x in (None, 0, 0.0, -0.0, 0.25, -2, 1e-40)] == [0, 0, 0, 0, 0.25, -2, 1e-40]
+    for scale in (None, 0, 0.25, -2, 1e-40, torch.tensor(0.5)):
+        fast.host.host_reset(0)
+        a = CALLS[0][1]
+        assert fast.linear_decode(*a[:5], scale, *a[6:]) is not None and fast.host.host_calls() == 1
