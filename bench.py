@@ -71,26 +71,30 @@ KERNEL_SOURCES = ["gated_delta_rule_55_amd/csrc/kda_prefill.hip",
                   "gated_delta_rule_55_amd/csrc/kda_conv.hip",
                   "gated_delta_rule_55_amd/csrc/kda_chunk_ops.h",
                   "gated_delta_rule_55_amd/csrc/kda_decode.hip",
-                  "gated_delta_rule_55_amd/csrc/kda_device.h",
-                  "gated_delta_rule_55_amd/build.py"]  # its flags shape the kernels too
+                  "gated_delta_rule_55_amd/csrc/kda_device.h"]
 
 
-def _code_only(rel: str, text: str) -> str:
-    """The HIP sources without their comments and with every run of white space
-    read as one space (a comment or layout edit does not change a kernel, so it
-    must not retire the counters taken on it)."""
-    if not rel.endswith((".hip", ".h")):
-        return text
+def _code_only(text: str) -> str:
+    """A HIP source without its comments and with every run of white space read
+    as one space (a comment or layout edit does not change a kernel, so it must
+    not retire the counters taken on it)."""
     text = re.sub(r"/\*.*?\*/", " ", text, flags=re.S)
     text = re.sub(r"//[^\n]*", " ", text)
     return re.sub(r"\s+", " ", text).strip()
 
 
 def kernel_source_hash() -> str:
+    """Of what makes the benched kernels: their sources and headers, and the
+    compile flags of each (without the include paths)."""
+    from gated_delta_rule_55_amd import build
+
     h = hashlib.sha256()
     for rel in KERNEL_SOURCES:
         with open(os.path.join(ROOT, rel), encoding="utf-8") as f:
-            h.update(_code_only(rel, f.read()).encode())
+            h.update(_code_only(f.read()).encode())
+        if rel.endswith(".hip"):
+            flags = build.HIPCC_FLAGS + build.SOURCE_FLAGS.get(os.path.basename(rel), [])
+            h.update(" ".join(x for x in flags if not x.startswith("-I")).encode())
     return h.hexdigest()[:16]
 
 
