@@ -1,11 +1,15 @@
 """Build libkda.so (HIP kernels + C ABI) for gfx950 with hipcc, and the Python
-module _fast.so on top of it, in-tree.
+module _fast.so on top of it, in-tree.  The library takes hipcc alone; where the
+module's tools are missing (g++, the headers of Python and torch) it is left out
+and layer.py makes every call itself.
 
 Usage: python -m gated_delta_rule_55_amd.build [-v]
 """
 import os
+import shutil
 import subprocess
 import sys
+import sysconfig
 import time
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -42,12 +46,31 @@ SOURCE_FLAGS = {
 FAST_OUT = os.path.join(PKG, "_fast.so")
 
 
-def _fast_command():
-    import sysconfig
+def _torch_root():
+    try:
+        import torch
+    except ImportError:
+        return None
+    return os.path.dirname(torch.__file__)
 
+
+def _fast_missing():
+    """What the module cannot be built without and is not here, or ''."""
+    if shutil.which("g++") is None:
+        return "g++"
+    if not os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        return "Python.h"
+    troot = _torch_root()
+    if troot is None or not os.path.exists(os.path.join(troot, "include", "torch", "csrc", "autograd",
+                                                        "python_variable.h")):
+        return "torch's headers"
+    return ""
+
+
+def _fast_command():
     import torch
 
-    troot = os.path.dirname(torch.__file__)
+    troot = _torch_root()
     rocm = os.environ.get("ROCM_PATH", "/opt/rocm")
     include = [f"-I{INCLUDE}"] + [f"-isystem{d}" for d in (
         os.path.join(troot, "include"), os.path.join(troot, "include", "torch", "csrc", "api", "include"),
@@ -62,6 +85,23 @@ def _fast_command():
 def _hipcc():
     p = os.path.join(os.environ.get("ROCM_PATH", "/opt/rocm"), "bin", "hipcc")
     return p if os.path.exists(p) else "hipcc"
+
+
+def build_fast(verbose: bool = False):
+    """Builds the module on top of the built library; its path, or None where its
+    tools are missing (an older one would not fit the library and goes)."""
+    missing = _fast_missing()
+    if missing:
+        print(f"{os.path.basename(FAST_OUT)} not built ({missing} not found): layer calls go through ctypes", flush=True)
+        if os.path.exists(FAST_OUT):
+            os.remove(FAST_OUT)
+        return None
+    cmd = _fast_command()
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True)
+    os.replace(FAST_OUT + ".tmp", FAST_OUT)
+    return FAST_OUT
 
 
 def build(verbose: bool = False, jobs: int = 4) -> str:
@@ -97,11 +137,7 @@ def build(verbose: bool = False, jobs: int = 4) -> str:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
     os.replace(OUT + ".tmp", OUT)
-    cmd = _fast_command()
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    subprocess.run(cmd, check=True)
-    os.replace(FAST_OUT + ".tmp", FAST_OUT)
+    build_fast(verbose)
     if verbose:
         print(f"built {OUT} in {time.time() - t0:.1f}s", flush=True)
     return OUT
