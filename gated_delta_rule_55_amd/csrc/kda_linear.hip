@@ -1,9 +1,9 @@
 // kda_linear.hip -- linear attention with one decay per head over packed
 // sequences (kda_linear_prefill).
 //
-// In chunks of 64 tokens (32 in fp32 and for short sequences), with G_i the sum of
-// the log-decays of a chunk's tokens up to and with i, G the whole chunk's and S
-// the state before it:
+// In chunks of 64 tokens (32 in fp32, and in bf16 where a launch of few tokens a
+// sequence splits none), with G_i the sum of the log-decays of a chunk's tokens
+// up to and with i, G the whole chunk's and S the state before it:
 //     o_i = scale (exp(G_i) S^T q_i + sum_{j <= i} exp(G_i - G_j) (q_i . k_j) v_j)
 //     S  <- exp(G) S + sum_j exp(G - G_j) k_j v_j^T
 // Every factor is at most 1 when g <= 0.  The chunks of a sequence follow one
@@ -28,12 +28,19 @@
 // would bring o's error from 2.3e-3 to the 1.7e-3 of its own rounding, at 430 us
 // against 396 for 32,768 tokens x 32 heads of 128.)
 //
-// What bounds it: the memory.  At that size pass 3 takes 247 us for 1.1 GB, at
-// 4.5 TB/s near a copy's 4.75, and 239 us with every product left out; pass 1
-// 130 us for the 0.5 GB of k and v, near the 4.0 TB/s of plain reading; pass 2
-// 12 us.  What that leaves is k and v read twice: the segments' states are the
-// price of 512 workgroups for 32 chains, and no order of the passes kept
-// half a gigabyte in the 256 MB cache.
+// What bounds it: the memory.  Of 32,768 tokens x 32 heads of 128 a kernel trace
+// gives pass 1 141 us for the 0.57 GB that it moves, the rate of plain reading
+// (4.0 TB/s), pass 2 13 us, and pass 3 265 us for 1.16 GB, at 4.4 TB/s near a
+// copy's 4.75; the passes of an untraced call take 393 us together.  (With every
+// product left out pass 3 took 239 us where it took 247 with them.)  What that
+// leaves is k and v read twice: the segments' states are the price of 512
+// workgroups for 32 chains.  Pass 3 in reverse order of segments, and the three
+// passes over groups of heads, did not bring k and v back from the 256 MB cache;
+// passes over blocks of tokens were not tried.
+//
+// Short calls are bound by the chain of their launches and chunks instead: one
+// sequence of 32 heads of 128 takes 19 us for 256 tokens, 34 for 1,024, 46 for
+// 2,048 and 79 for 4,096, which a copy would move in 3, 8, 15 and 29.
 #include <type_traits>
 
 #include "kda_enqueue.h"
@@ -318,6 +325,14 @@ __device__ __forceinline__ double decay_sums(Decays<C>& d, float g, bool head, i
   return all;
 }
 
+// Registers: __launch_bounds__ caps three output passes of bf16 where they spill a little
+// (two heads of 64 a workgroup, dk 128: 2 of them in chunks of 64, 16 in chunks
+// of 32; heads of 128 x 128 in chunks of 32: 3), for one more workgroup a CU.
+// Workgroups of one or two waves, for heads of 32 and 64 that are not grouped,
+// hold a whole dk x 32 state a wave and Q and K for themselves alone: with heads
+// of 128 x 32 in bf16 a CU has room for three waves (8,192 tokens x 32 heads 98
+// us; four heads to a key head, grouped, 59).
+//
 // Passes 1 (OUT = false) and 3 (OUT = true).  A workgroup walks one segment
 // for HG heads that share a key head: VW value columns in all, 32 a wave.
 // 64 sequences of 1,024 tokens, heads of 128 x 64, eight to a key head: 250 us
@@ -701,7 +716,10 @@ hipError_t launch(const LinearParams& p, bool split, hipStream_t stream) {
   // Sequences of few tokens in bf16 are mostly loads and stores of states: chunks
   // of 32 leave room for three workgroups a CU (24 sequences of 851 tokens in all,
   // 32 heads of 128: 20 us against 24).  Longer ones lose a little by it (64 x
-  // 1,024 tokens: 267 us against 256).
+  // 1,024 tokens: 267 us against 256).  That is asked of the batch's average, and
+  // only where no sequence can be split: a batch of more tokens than a segment
+  // (1,024 from 256 sequences x heads on) runs all three passes in chunks of 64,
+  // however short its sequences are (64 x 20 tokens: 54 us, a copy's time 37).
   if constexpr (sizeof(T) == 2) {
     if (!split && p.T <= 64 * (int64_t)p.N)
       return enqueue(linear_kernel<T, 32, DK, VW, HG, true>, (unsigned)blocks, 2 * VW, stream, p);
@@ -740,7 +758,9 @@ int64_t linear_segment(int64_t t_total, int n_seqs, int n_heads, int dv, bool bf
   // about eight waves, of 32 value columns each, for each of the 256 CUs (one
   // sequence of 32,768 tokens x 32 heads: 400 us, with twelve 455, sixteen 424);
   // for several sequences, whose segments are not equally long, twelve (eight of
-  // 33,001 tokens in all: 395 us, with eight or sixteen 455 to 460)
+  // 33,001 tokens in all: 395 us, with eight or sixteen 455 to 460).  Steps of
+  // that size come from how segments fill the last round of 512 workgroups; other
+  // lengths may do better with another number.
   const int64_t waves = 256 * (n_seqs == 1 ? 8 : 12);
   const int64_t want = (t_total * n_heads * (dv / 32) + waves - 1) / waves;
   int64_t seg = (want + kGrain - 1) / kGrain * kGrain;

@@ -12,7 +12,9 @@
 //
 // Bound by the memory: 1 M rows of 128 in bf16 with a gate, 805 MB, 147 us
 // (5.5 TB/s, above a copy's 4.75: two reads to a write); 32,768 rows of 4,096
-// around a block with every option, 1.34 GB, 249 us (5.4 TB/s).  Rows of 4,097,
+// around a block with every option, 1.34 GB, 245 us (5.5 TB/s), as a plain add and
+// norm, 1.07 GB, 187 us (5.7).  In fp32 half as many rows are the same bytes: 159
+// us for the gate, 251 and 195 around a block.  Rows of 4,097,
 // whose vectors are not aligned, run at 4.1 to 4.9 TB/s.
 #include "kda_device.h"
 #include "kda_enqueue.h"
@@ -232,9 +234,11 @@ __global__ __launch_bounds__(threads_of<TPR>()) void block_norm_kernel(BlockNorm
 // vectors each (a block norm holds five operands of each in registers), four
 // where 1,024 threads do not go round otherwise.  (16,384 columns are 2,048
 // vectors of bf16 and 4,096 of fp32.)  Up to 512 rows leave the chip half empty
-// and the time is one row's: then one vector each, up to 512 threads (64 rows of
-// 4,096 in bf16, gated norm 3.6 -> 3.3 us, block norm 4.1 -> 3.8; from 1,024 rows
-// on it is the slower, 6.2 -> 6.6 and 10.6 -> 11.2).
+// and the time is one row's: then one vector each, up to 512 threads (rows of
+// 4,096 in bf16 with a gate, and around a block with every option and an fp32
+// residual, one vector against two: 64 rows 3.3 against 3.7 us and 4.4 against
+// 4.8, 512 rows 4.4 against 4.6 and 7.2 against 7.5; 1,024 rows 6.6 against 7.1
+// and 11.9 against 11.3).
 template <typename T, typename L>
 hipError_t dispatch(int64_t rows, int nvec, const L& l) {
   if (nvec <= 8) return l.template run<8, 1>();
