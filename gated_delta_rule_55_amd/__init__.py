@@ -2,7 +2,8 @@
 recurrent decode, and the short causal conv before them, as hand-written HIP
 kernels behind a C ABI (include/kda.h, include/kda_conv.h); linear attention
 with a decay per head (include/kda_linear.h) and the norms of a layer around
-either (include/kda_norm.h)."""
+either (include/kda_norm.h); latent attention over a paged cache, for the layers
+between them (include/kda_latent.h)."""
 from .kda import (  # noqa: F401
     causal_conv1d_fwd,
     causal_conv1d_update,
@@ -11,6 +12,15 @@ from .kda import (  # noqa: F401
     recurrent_decode,
     recurrent_prefill,
     workspace_status,
+)
+from .latent import (  # noqa: F401
+    latent_append,
+    latent_decode,
+    latent_extend,
+    latent_prefill,
+    latent_workspace_bytes,
+    rotary,
+    rotary_frequencies,
 )
 from .layer import (  # noqa: F401
     block_norm,

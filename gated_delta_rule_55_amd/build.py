@@ -17,7 +17,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT = os.path.join(PKG, "libkda.so")
-SOURCES = ["kda_abi.cpp", "kda_conv.hip", "kda_decode.hip", "kda_headscan.hip", "kda_linear.hip",
+SOURCES = ["kda_abi.cpp", "kda_conv.hip", "kda_decode.hip", "kda_headscan.hip", "kda_latent_abi.cpp",
+           "kda_latent_attend.hip", "kda_latent_cache.hip", "kda_latent_prefill.hip", "kda_linear.hip",
            "kda_linear_abi.cpp", "kda_linear_decode.hip", "kda_norm.hip", "kda_norm_abi.cpp",
            "kda_prefill.hip"]
 ARCH = "gfx950"

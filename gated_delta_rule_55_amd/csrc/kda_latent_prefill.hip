@@ -1,0 +1,265 @@
+// kda_latent_prefill.hip -- expanded latent attention over packed prompts
+// (kda_latent_prefill): o_i = sum_j p_ij v_j with p_ij the softmax over the keys
+// j <= i + Lk - Lq of scale (q_i[:dn] . k_j + q_i[dn:] . k_pe_j).
+//
+// A workgroup takes 128 queries of one head, 32 to a wave, and walks the keys in
+// tiles of 64 that all four waves read from LDS: scores transposed (S^T = K Q^T,
+// a query per lane), the running maximum m and sum l of the softmax in fp32, and
+// O^T += V^T P^T with the weights straight from the score registers.  O is scaled
+// by 2^(m_old - m_new) where a maximum grew.
+#include "kda_enqueue.h"
+#include "kda_latent_launch.h"
+#include "kda_latent_ops.h"
+
+namespace kda {
+namespace {
+
+constexpr int QB = kLatentQueryBlock, KB = 64, THREADS = 256;
+
+// Keys, positional parts and values of a tile, each in whole column blocks.
+template <typename T, int DN, int DR, int DV>
+struct Tile {
+  static constexpr int ES = sizeof(T);
+  static constexpr int kn = DN * ES / 128, kp = (DR * ES + 127) / 128, kv = DV * ES / 128;
+  static constexpr int pe = kn * KB * 128, v = pe + kp * KB * 128, bytes = v + kv * KB * 128;
+  static constexpr int loads = 2 * (kn + kp + kv);  // 16-byte loads a thread makes
+  // positional rows narrower than a column block: these lanes have none of it
+  static __device__ __forceinline__ bool in_pe(int block, int chunk) { return (8 * block + chunk) * 16 < DR * ES; }
+};
+
+template <typename T, int DN, int DR, int DV>
+struct Prefill {
+  using L = Tile<T, DN, DR, DV>;
+  using F = typename Frag<T>::type;
+  static constexpr int KS = (DN + DR) / 16, NV = DV / 32;
+
+  F q[KS];
+  f32x16 o[NV];
+  float m, l;
+
+  // One tile's keys from position `key0` on, of which this lane's query sees those
+  // up to `last`.  MASKED: some query of the wave does not see all of them.
+  template <bool MASKED>
+  __device__ __forceinline__ void step(const char* lds, int key0, int last, float c, int lane) {
+    const int h = lane >> 5;
+    f32x16 s[2] = {zero16(), zero16()};
+#pragma unroll
+    for (int k = 0; k < KS; ++k)
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const int row = 32 * t + (lane & 31), col = 16 * k + 8 * h;
+        s[t] = mma16(16 * k < DN ? tile_row8<KB>(lds, row, col, T()) : tile_row8<KB>(lds + L::pe, row, col - DN, T()),
+                     q[k], s[t]);
+      }
+    if (MASKED) {
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (key0 + 32 * t + row_of(h, i) > last) s[t][i] = -__builtin_inff();
+    }
+    float top = m;
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) top = fmaxf(top, s[t][i]);
+    top = fmaxf(top, other_half(top));
+    const float base = top == -__builtin_inff() ? 0.f : top * c;
+    const float alpha = fast_exp2(m * c - base);
+    m = top;
+    float sum = 0.f;
+    F p[4];
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float x = fast_exp2(s[t][i] * c - base);
+        sum += x;
+        p[2 * t + (i >> 3)][i & 7] = from_f32<T>(x);  // bf16: one rounding, 2^-8
+      }
+    l = l * alpha + sum;
+    if (__any(alpha != 1.f)) {
+#pragma unroll
+      for (int d = 0; d < NV; ++d) o[d] *= alpha;
+    }
+    const char* values = lds + L::v;
+    if (MASKED && special(values, lane)) {
+      values_special(values, p, key0, last, lane);
+      return;
+    }
+#pragma unroll
+    for (int d = 0; d < NV; ++d)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) o[d] = mma16(tile_col8<KB>(values, 16 * k, 32 * d, lane, T()), p[k], o[d]);
+  }
+
+  // Whether a tile holds a value that is not finite.
+  static __device__ __forceinline__ bool special(const char* values, int lane) {
+    bool any = false;
+#pragma unroll
+    for (int b = 0; b < L::kv * KB * 128 / 1024; ++b) {
+      const uint4 x = *reinterpret_cast<const uint4*>(values + b * 1024 + lane * 16);
+      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (sizeof(T) == 2)
+          any |= (w[i] & 0x7f80u) == 0x7f80u || (w[i] & 0x7f800000u) == 0x7f800000u;
+        else
+          any |= (w[i] & 0x7f800000u) == 0x7f800000u;
+      }
+    }
+    return __any(any);
+  }
+  __device__ __forceinline__ void values_special(const char* values, const F (&p)[4], int key0, int last, int lane) {
+    const int h = lane >> 5;
+#pragma unroll
+    for (int d = 0; d < NV; ++d) {
+      f32x16 kinds = zero16();
+#pragma unroll 1
+      for (int k = 0; k < 4; ++k) {
+        F v = tile_col8<KB>(values, 16 * k, 32 * d, lane, T()), kind, sees, w;
+        split_special(v, kind);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          sees[e] = from_f32<T>(key0 + 16 * k + 8 * (e >> 2) + 4 * h + (e & 3) <= last ? 1.f : 0.f);
+        w = k == 0 ? p[0] : k == 1 ? p[1] : k == 2 ? p[2] : p[3];
+        o[d] = mma16(v, w, o[d]);
+        kinds = mma16(kind, sees, kinds);
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) o[d][i] = add_special(o[d][i], kinds[i]);
+    }
+  }
+};
+
+template <typename T, int DN, int DR, int DV>
+__global__ __launch_bounds__(THREADS, 2) void latent_prefill_kernel(LatentPrefillArgs a, int blocks, int classes) {
+  using P = Prefill<T, DN, DR, DV>;
+  using L = Tile<T, DN, DR, DV>;
+  constexpr int ES = sizeof(T);
+  __shared__ __attribute__((aligned(128))) char lds[L::bytes];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, h = lane >> 5;
+
+  // Workgroups go round the 8 XCDs; those of one XCD take the heads of one class, a
+  // head after the other, so that the workgroups that run together there read the
+  // same keys through its L2.  Late queries, which see most keys, go first.
+  const int xcd = blockIdx.x & 7, per = 8 / classes, i = blockIdx.x >> 3;
+  const int nb = (blocks + per - 1) / per;
+  const int head = xcd / per + classes * (i / nb);
+  const int back = xcd % per + per * (i % nb);
+  if (back >= blocks) return;
+  const int64_t b = blocks - 1 - back;
+  const int n = find_sequence<QB>(a.cu, a.n_seqs, a.q_total, 1, b);
+  const int q0 = a.cu ? seq_start(a.cu, n, a.q_total) : 0, q1 = a.cu ? seq_start(a.cu, n + 1, a.q_total) : a.q_total;
+  const int64_t block = b - first_block<QB>(q0, 1, n);
+  if (block < 0 || block * QB >= q1 - q0) return;
+  const int32_t* cu_k = a.cu_k ? a.cu_k : a.cu;
+  const int k0 = cu_k ? seq_start(cu_k, n, a.k_total) : 0, k1 = cu_k ? seq_start(cu_k, n + 1, a.k_total) : a.k_total;
+  const int keys = max(k1 - k0, 0), queries = q1 - q0;
+  const int first = (int)block * QB, mine = first + 32 * wave + (lane & 31);
+  const int last = mine + (keys - queries);                     // the last key this lane's query sees
+  const int wave_last = first + 32 * wave + (keys - queries);   // the last one that all of the wave's see
+  // keys that the workgroup's last query sees
+  const int end = min(first + QB, queries) + (keys - queries);
+
+  P s;
+  {
+    const char* row = static_cast<const char*>(a.q) +
+                      ((int64_t)(q0 + min(mine, queries - 1)) * a.q_stride + (int64_t)head * (DN + DR) + 8 * h) * ES;
+#pragma unroll
+    for (int k = 0; k < P::KS; ++k) s.q[k] = load_frag8<T>(reinterpret_cast<const T*>(row + 16 * k * ES));
+  }
+#pragma unroll
+  for (int d = 0; d < P::NV; ++d) s.o[d] = zero16();
+  s.m = -__builtin_inff();
+  s.l = 0.f;
+
+  // This thread's part of a tile: 16 bytes of two rows in each column block.
+  const int chunk = lane & 7, r0 = 16 * wave + (lane >> 3);
+  const float c = a.scale * kLog2e;
+  uint4 st[L::loads];
+  auto load = [&](int tile) {
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int j = tile * KB + r0 + 8 * r;
+      const bool in = j < keys;  // rows past the sequence are 0: another sequence's, or nobody's
+      const int64_t at = k0 + (in ? j : 0);
+      const char* kr = static_cast<const char*>(a.k) + (at * a.k_stride + head * a.k_head) * ES + chunk * 16;
+      const char* pr = static_cast<const char*>(a.pe) + at * a.pe_stride * ES + chunk * 16;
+      const char* vr = static_cast<const char*>(a.v) + (at * a.v_stride + head * a.v_head) * ES + chunk * 16;
+      const uint4 none = {0, 0, 0, 0};
+#pragma unroll
+      for (int x = 0; x < L::kn; ++x) st[r * L::loads / 2 + x] = in ? *reinterpret_cast<const uint4*>(kr + 128 * x) : none;
+#pragma unroll
+      for (int x = 0; x < L::kp; ++x)
+        st[r * L::loads / 2 + L::kn + x] = in && L::in_pe(x, chunk) ? *reinterpret_cast<const uint4*>(pr + 128 * x) : none;
+#pragma unroll
+      for (int x = 0; x < L::kv; ++x)
+        st[r * L::loads / 2 + L::kn + L::kp + x] = in ? *reinterpret_cast<const uint4*>(vr + 128 * x) : none;
+    }
+  };
+  const int tiles = end > 0 ? (end + KB - 1) / KB : 0;
+  if (tiles > 0) load(0);
+  for (int t = 0; t < tiles; ++t) {
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+      for (int x = 0; x < L::loads / 2; ++x)
+        *reinterpret_cast<uint4*>(lds + x * KB * 128 + tile_at<KB>(r0 + 8 * r, chunk * 16)) = st[r * L::loads / 2 + x];
+    __syncthreads();
+    if (t + 1 < tiles) load(t + 1);
+    if (t * KB + KB - 1 <= wave_last)
+      s.template step<false>(lds, t * KB, last, c, lane);
+    else if (t * KB <= wave_last + 31)
+      s.template step<true>(lds, t * KB, last, c, lane);
+  }
+
+  if (mine >= queries) return;
+  const float sum = s.l + other_half(s.l);
+  const float inv = last >= 0 ? 1.f / sum : 0.f;  // no key: O is 0
+  T* row = static_cast<T*>(a.o) + (int64_t)(q0 + mine) * a.o_stride + (int64_t)head * DV;
+#pragma unroll
+  for (int d = 0; d < P::NV; ++d)
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      typename Vec4<T>::type y;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) y[e] = from_f32<T>(s.o[d][4 * g + e] * inv);
+      *reinterpret_cast<typename Vec4<T>::type*>(row + 32 * d + 8 * g + 4 * h) = y;
+    }
+}
+
+template <typename T, int DN, int DR, int DV>
+hipError_t run(const LatentPrefillArgs& a, hipStream_t stream) {
+  const int64_t blocks = latent_query_blocks(a.q_total, a.n_seqs);
+  int classes = 1;  // of heads: the XCDs share them evenly
+  while (classes < 8 && a.n_heads % (2 * classes) == 0) classes *= 2;
+  const int64_t per = 8 / classes;
+  const int64_t grid = 8 * ((blocks + per - 1) / per) * (a.n_heads / classes);
+  return enqueue(latent_prefill_kernel<T, DN, DR, DV>, (unsigned)grid, THREADS, stream, a, (int)blocks, classes);
+}
+
+template <typename T, int DN, int DR>
+hipError_t by_dv(const LatentPrefillArgs& a, hipStream_t stream) {
+  return a.dv == 128 ? run<T, DN, DR, 128>(a, stream) : run<T, DN, DR, 64>(a, stream);
+}
+
+template <typename T, int DN>
+hipError_t by_dr(const LatentPrefillArgs& a, hipStream_t stream) {
+  return a.dr == 64 ? by_dv<T, DN, 64>(a, stream) : by_dv<T, DN, 32>(a, stream);
+}
+
+template <typename T>
+hipError_t by_dn(const LatentPrefillArgs& a, hipStream_t stream) {
+  return a.dn == 128 ? by_dr<T, 128>(a, stream) : by_dr<T, 64>(a, stream);
+}
+
+}  // namespace
+
+hipError_t launch_latent_prefill(const LatentPrefillArgs& a, hipStream_t stream) {
+  if (a.q_total == 0) return hipSuccess;
+  return a.bf16 ? by_dn<bf16>(a, stream) : by_dn<float>(a, stream);
+}
+
+}  // namespace kda
