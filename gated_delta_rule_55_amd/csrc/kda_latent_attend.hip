@@ -52,7 +52,8 @@ struct Workspace {
 
 // What a call's sequence holds.
 struct Sequence {
-  int start, tokens, rows;  // first new token; new tokens; rows of the cache
+  int start, tokens;        // first new token; new tokens
+  int length, rows;         // seq_lens, and the rows of it that the table has places for
   int64_t units;
   int tiles;  // of each unit (one at least)
 };
@@ -60,7 +61,8 @@ __device__ __forceinline__ Sequence sequence_of(const LatentPages& g, int n_head
   Sequence s;
   s.start = seq_start(g.cu, n, g.t_total);
   s.tokens = max((g.cu ? seq_start(g.cu, n + 1, g.t_total) : n + 1) - s.start, 0);
-  s.rows = min(max(g.lens[n], 0), g.max_pages * g.page_size);
+  s.length = max(g.lens[n], 0);
+  s.rows = min(s.length, g.max_pages * g.page_size);
   s.units = ((int64_t)s.tokens * n_heads + ROWS - 1) / ROWS;
   s.tiles = max((s.rows + KB - 1) / KB, 1);
   return s;
@@ -166,7 +168,7 @@ __global__ __launch_bounds__(THREADS, 1) void latent_attend_kernel(LatentAttendA
     const int row0 = unit * ROWS, n_rows = s.tokens * a.n_heads;
     const auto limit_of = [&](int r) {
       const int tok = min(row0 + r, n_rows - 1) / a.n_heads;
-      return min(max(s.rows + tok + 1 - s.tokens, 0), s.rows);
+      return min(max(s.length + (tok + 1 - s.tokens), 0), s.rows);
     };
     const int most = limit_of(ROWS - 1), least = limit_of(0);
     F q[NT][KS];
@@ -249,8 +251,8 @@ __global__ __launch_bounds__(THREADS, 1) void latent_attend_kernel(LatentAttendA
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         const float m = tops_of(16 * t + col, top[t]);
-        const float base = m == -__builtin_inff() ? 0.f : m * c;
-        sum[t] *= fast_exp2(top[t] * c - base);
+        const float base = m == -__builtin_inff() ? 0.f : __fmul_rn(m, c);
+        sum[t] *= fast_exp2(__fmul_rn(top[t], c) - base);
         top[t] = m;
         typename Vec4<T>::type p;
 #pragma unroll
@@ -262,7 +264,7 @@ __global__ __launch_bounds__(THREADS, 1) void latent_attend_kernel(LatentAttendA
         *reinterpret_cast<typename Vec4<T>::type*>(weights + (16 * t + col) * S::p_row + (16 * wave + 4 * grp) * ES) = p;
       }
       const float m = tops_of(lane & 31, top_o);
-      const float alpha = fast_exp2(top_o * c - (m == -__builtin_inff() ? 0.f : m * c));
+      const float alpha = fast_exp2(__fmul_rn(top_o, c) - (m == -__builtin_inff() ? 0.f : __fmul_rn(m, c)));
       top_o = m;
       if (__any(alpha != 1.f)) {
 #pragma unroll
@@ -391,7 +393,7 @@ __global__ __launch_bounds__(DC / 4) void latent_join_kernel(LatentAttendArgs a,
     const float2 st = ws.stats[place(i)];
     if (!(st.y == -1.f)) top = fmaxf(top, st.x);
   }
-  const float base = top == -__builtin_inff() ? 0.f : top * c;
+  const float base = top == -__builtin_inff() ? 0.f : __fmul_rn(top, c);
   f32x4 o = zero4();
   float sum = 0.f;
   bool some = false;
@@ -399,7 +401,7 @@ __global__ __launch_bounds__(DC / 4) void latent_join_kernel(LatentAttendArgs a,
     const float2 st = ws.stats[place(i)];
     if (st.y == -1.f) continue;
     some = true;
-    const float f = fast_exp2(st.x * c - base);
+    const float f = fast_exp2(__fmul_rn(st.x, c) - base);
     sum += f * st.y;
     o += f * *reinterpret_cast<const f32x4*>(ws.sums + place(i) * DC + 4 * threadIdx.x);
   }

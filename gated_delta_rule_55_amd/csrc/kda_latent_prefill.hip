@@ -64,8 +64,9 @@ struct Prefill {
 #pragma unroll
       for (int i = 0; i < 16; ++i) top = fmaxf(top, s[t][i]);
     top = fmaxf(top, other_half(top));
-    const float base = top == -__builtin_inff() ? 0.f : top * c;
-    const float alpha = fast_exp2(m * c - base);
+    // (a maximum's product with c is rounded the same way each time it is formed)
+    const float base = top == -__builtin_inff() ? 0.f : __fmul_rn(top, c);
+    const float alpha = fast_exp2(__fmul_rn(m, c) - base);
     m = top;
     float sum = 0.f;
     F p[4];

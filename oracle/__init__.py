@@ -12,6 +12,7 @@ it.  Contents:
   heads.py                      q/k L2 normalisation, grouped key heads (fp64)
   linear.py                     linear attention with a decay per head (fp64)
   norm.py                       gated and block norms (fp64)
+  latent.py                     latent attention, its cache rows, the rotation (fp64)
 """
 from .recurrent import (OracleLib, decode, lib_path, num_threads, prefill,  # noqa: F401
                         prefill_f32, set_num_threads)
@@ -21,3 +22,5 @@ from .conv import causal_conv1d, silu  # noqa: F401
 from .heads import L2NORM_EPS, expand_key_heads, l2norm  # noqa: F401
 from .linear import linear_attention, linear_decode  # noqa: F401
 from .norm import block_norm, gated_norm, rmsnorm  # noqa: F401
+from .latent import (attend, latent_attend, latent_new_rows, latent_prefill, latent_rows,  # noqa: F401
+                     rotary)
