@@ -21,6 +21,7 @@ using kda::row_set;
 using kda::RowSet;
 
 constexpr int64_t kMaxStride = (int64_t)1 << 28;
+constexpr int64_t kMaxKeyStride = (int64_t)1 << 22;
 constexpr int64_t kMaxTokens = INT32_MAX - 64;
 // Workgroups of a launch: threads stay below 2^32.
 constexpr int64_t kMaxBlocks = (int64_t)1 << 23;
@@ -154,6 +155,8 @@ int kda_latent_prefill(const kda_latent_prefill_desc* d, void* stream) {
   for (const void* p : p16)
     if (!aligned(p, 16)) return KDA_ERR_ALIGN;
   if (!aligned(d->cu_seqlens, 4) || !aligned(d->cu_seqlens_k, 4)) return KDA_ERR_ALIGN;
+  // keeps the byte offsets of a tile of 64 keys in 31 bits
+  if (a.k_stride > kMaxKeyStride || a.pe_stride > kMaxKeyStride || a.v_stride > kMaxKeyStride) return KDA_ERR_SHAPE;
   const RowSet o = row_set(d->o, T, a.o_stride, H * dv, es);
   const RowSet ins[] = {row_set(d->q, T, a.q_stride, H * (dn + dr), es),
                         head_rows(d->k, K, a.k_stride, H, a.k_head, dn, es), row_set(d->k_pe, K, a.pe_stride, dr, es),

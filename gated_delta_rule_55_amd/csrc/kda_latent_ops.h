@@ -115,6 +115,24 @@ __device__ __forceinline__ float add_special(float acc, float kinds) {
   return acc;
 }
 
+// 16 bytes from each lane's place in the buffer to 1,024 consecutive bytes of LDS,
+// without passing through registers; a lane whose place lies outside the buffer
+// writes 0.  `at` is the wave's own part of LDS.  What is fetched is there once the
+// wave has waited (fetched()).  The compiler orders LDS reads behind a fetch into
+// the same array only, so what is read while a fetch is under way is an array of its
+// own.
+__device__ __forceinline__ void fetch16(__amdgpu_buffer_rsrc_t r, int place, int uniform, char* at) {
+  typedef __attribute__((address_space(3))) void* lds;
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds)at, 16, place, uniform, 0, 0);
+}
+// Waits for this wave's fetches and LDS accesses, then for the workgroup's other waves.
+__device__ __forceinline__ void fetched() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
 // Values of the other half of the wave (lane l ^ 32).
 __device__ __forceinline__ float other_half(float x) { return __shfl_xor(x, 32); }
 

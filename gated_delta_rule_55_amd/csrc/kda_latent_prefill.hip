@@ -22,9 +22,6 @@ struct Tile {
   static constexpr int ES = sizeof(T);
   static constexpr int kn = DN * ES / 128, kp = (DR * ES + 127) / 128, kv = DV * ES / 128;
   static constexpr int pe = kn * KB * 128, v = pe + kp * KB * 128, bytes = v + kv * KB * 128;
-  static constexpr int loads = 2 * (kn + kp + kv);  // 16-byte loads a thread makes
-  // positional rows narrower than a column block: these lanes have none of it
-  static __device__ __forceinline__ bool in_pe(int block, int chunk) { return (8 * block + chunk) * 16 < DR * ES; }
 };
 
 template <typename T, int DN, int DR, int DV>
@@ -134,11 +131,11 @@ struct Prefill {
 };
 
 template <typename T, int DN, int DR, int DV>
-__global__ __launch_bounds__(THREADS, 2) void latent_prefill_kernel(LatentPrefillArgs a, int blocks, int classes) {
+__global__ __launch_bounds__(THREADS, sizeof(T) == 2 ? 2 : 1) void latent_prefill_kernel(LatentPrefillArgs a, int blocks, int classes) {
   using P = Prefill<T, DN, DR, DV>;
   using L = Tile<T, DN, DR, DV>;
   constexpr int ES = sizeof(T);
-  __shared__ __attribute__((aligned(128))) char lds[L::bytes];
+  __shared__ __attribute__((aligned(128))) char even[L::bytes], odd[L::bytes];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, h = lane >> 5;
 
   // Workgroups go round the 8 XCDs; those of one XCD take the heads of one class, a
@@ -175,45 +172,52 @@ __global__ __launch_bounds__(THREADS, 2) void latent_prefill_kernel(LatentPrefil
   s.m = -__builtin_inff();
   s.l = 0.f;
 
-  // This thread's part of a tile: 16 bytes of two rows in each column block.
-  const int chunk = lane & 7, r0 = 16 * wave + (lane >> 3);
+  // The next tile is fetched while one is worked on.  A wave fetches 16 rows of it,
+  // eight lanes to 128 bytes of a row, the chunks exchanged as tile_at has them.
   const float c = a.scale * kLog2e;
-  uint4 st[L::loads];
-  auto load = [&](int tile) {
+  const int r0 = 16 * wave + (lane >> 3), chunk = ((lane & 7) ^ (lane >> 3)) * 16;
+  const int k_row = (int)a.k_stride * ES, p_row = (int)a.pe_stride * ES, v_row = (int)a.v_stride * ES;
+  const char* kt = static_cast<const char*>(a.k) + (k0 * a.k_stride + head * a.k_head) * ES;
+  const char* pt = static_cast<const char*>(a.pe) + k0 * a.pe_stride * ES;
+  const char* vt = static_cast<const char*>(a.v) + (k0 * a.v_stride + head * a.v_head) * ES;
+  auto fetch = [&](int t, char* tile) {
+    // rows past the sequence, which are another's or nobody's, are 0
+    const int rows = min(keys - t * KB, KB) - 1;
+    const auto kr = make_rsrc(const_cast<char*>(kt + (int64_t)t * KB * k_row), rows * k_row + DN * ES);
+    const auto pr = make_rsrc(const_cast<char*>(pt + (int64_t)t * KB * p_row), rows * p_row + DR * ES);
+    const auto vr = make_rsrc(const_cast<char*>(vt + (int64_t)t * KB * v_row), rows * v_row + DV * ES);
+    char* at = tile + 16 * wave * 128;
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      const int j = tile * KB + r0 + 8 * r;
-      const bool in = j < keys;  // rows past the sequence are 0: another sequence's, or nobody's
-      const int64_t at = k0 + (in ? j : 0);
-      const char* kr = static_cast<const char*>(a.k) + (at * a.k_stride + head * a.k_head) * ES + chunk * 16;
-      const char* pr = static_cast<const char*>(a.pe) + at * a.pe_stride * ES + chunk * 16;
-      const char* vr = static_cast<const char*>(a.v) + (at * a.v_stride + head * a.v_head) * ES + chunk * 16;
-      const uint4 none = {0, 0, 0, 0};
+      const int row = r0 + 8 * r;
 #pragma unroll
-      for (int x = 0; x < L::kn; ++x) st[r * L::loads / 2 + x] = in ? *reinterpret_cast<const uint4*>(kr + 128 * x) : none;
+      for (int x = 0; x < L::kn; ++x) fetch16(kr, row * k_row + chunk, 128 * x, at + (x * KB + 8 * r) * 128);
 #pragma unroll
-      for (int x = 0; x < L::kp; ++x)
-        st[r * L::loads / 2 + L::kn + x] = in && L::in_pe(x, chunk) ? *reinterpret_cast<const uint4*>(pr + 128 * x) : none;
+      for (int x = 0; x < L::kp; ++x) {
+        // a positional row narrower than a column block: the other lanes' chunks are not read
+        const bool in = 128 * x + chunk < DR * ES;
+        fetch16(pr, in ? row * p_row + chunk : kBufferOff, 128 * x, at + L::pe + (x * KB + 8 * r) * 128);
+      }
 #pragma unroll
-      for (int x = 0; x < L::kv; ++x)
-        st[r * L::loads / 2 + L::kn + L::kp + x] = in ? *reinterpret_cast<const uint4*>(vr + 128 * x) : none;
+      for (int x = 0; x < L::kv; ++x) fetch16(vr, row * v_row + chunk, 128 * x, at + L::v + (x * KB + 8 * r) * 128);
     }
   };
-  const int tiles = end > 0 ? (end + KB - 1) / KB : 0;
-  if (tiles > 0) load(0);
-  for (int t = 0; t < tiles; ++t) {
-    __syncthreads();
-#pragma unroll
-    for (int r = 0; r < 2; ++r)
-#pragma unroll
-      for (int x = 0; x < L::loads / 2; ++x)
-        *reinterpret_cast<uint4*>(lds + x * KB * 128 + tile_at<KB>(r0 + 8 * r, chunk * 16)) = st[r * L::loads / 2 + x];
-    __syncthreads();
-    if (t + 1 < tiles) load(t + 1);
+  auto work = [&](int t, const char* tile) {
     if (t * KB + KB - 1 <= wave_last)
-      s.template step<false>(lds, t * KB, last, c, lane);
+      s.template step<false>(tile, t * KB, last, c, lane);
     else if (t * KB <= wave_last + 31)
-      s.template step<true>(lds, t * KB, last, c, lane);
+      s.template step<true>(tile, t * KB, last, c, lane);
+  };
+  const int tiles = end > 0 ? (end + KB - 1) / KB : 0;
+  if (tiles > 0) fetch(0, even);
+  for (int t = 0; t < tiles; t += 2) {
+    fetched();
+    if (t + 1 < tiles) fetch(t + 1, odd);
+    work(t, even);
+    if (t + 1 == tiles) break;
+    fetched();
+    if (t + 2 < tiles) fetch(t + 2, even);
+    work(t + 1, odd);
   }
 
   if (mine >= queries) return;

@@ -56,6 +56,7 @@ extern "C" {
  * Layouts: q [q_total, H, dn + dr]; k [k_total, H, dn]; k_pe [k_total, dr];
  * v [k_total, H, dv]; o [q_total, H, dv].  k and v may be slices of one buffer
  * [k_total, H, dn + dv]: besides the token stride they have a head stride.
+ * The token strides of k, k_pe and v are at most 2^22, dense or not.
  * cu_seqlens [N + 1] gives the sequences' queries, cu_seqlens_k [N + 1] their
  * keys; NULL: the same as the queries' (k_total == q_total then).  Both are read
  * on the device, clamped to [0, q_total] and [0, k_total]: contents that break
