@@ -113,8 +113,8 @@ int check_attend(const kda_latent_attend_desc* d, kda::LatentAttendArgs* a) {
   if ((st = check_stride(d->q_stride, H * (d->dc + d->dr), es, &a->q_stride)) != KDA_OK ||
       (st = check_stride(d->o_stride, H * d->dc, es, &a->o_stride)) != KDA_OK)
     return st;
-  // units of 32 (token, head) rows, and a workgroup for each of their rows
-  if (d->t_total * H > INT32_MAX - 64 || d->t_total * H / 32 + (d->cu_seqlens ? 1 : (H + 31) / 32) * d->n_seqs >= kMaxBlocks / 2)
+  // (token, head) rows are counted in 32 bits
+  if (d->t_total * H > kMaxTokens)
     return KDA_ERR_SHAPE;
   a->bf16 = d->dtype == KDA_DTYPE_BF16;
   a->n_heads = d->n_heads;

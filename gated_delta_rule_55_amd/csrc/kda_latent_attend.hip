@@ -20,50 +20,60 @@
 namespace kda {
 namespace {
 
-constexpr int KB = 64, THREADS = 256, ROWS = 32;
-constexpr int RUNS = 256;      // workgroups: a tile of 64 x 576 in LDS leaves room for one per CU
-constexpr int MIN_TILES = 2;   // of a run
+constexpr int JOIN_THREADS = 256;
+constexpr int RUNS = 256;     // workgroups: their tiles in LDS leave room for one per CU
+constexpr int MIN_TILES = 2;  // of a run
 
-// Units of a call at most, and the workspace: a head per unit, then pieces.  A run
-// has at most two pieces of units that are cut: one that begins inside its unit
-// (place 2 run) and one that begins with it (2 run + 1).
+// The workspace.  A run has at most two pieces of units that are cut: one that begins
+// inside its unit (place 2 run) and one that begins with it (place 2 run + 1).  The
+// latter's head says where the unit's other pieces are.  Heads are numbered by unit
+// where a call has few of them, so that the join has a workgroup for each row and 128
+// columns of these and no idle ones, else by run, with fewer workgroups each.
+constexpr int FEW_UNITS = 64;
 struct Plan {
-  int64_t units;
-  int runs;
+  int rows;  // of a unit
+  bool by_unit;
+  int64_t units;  // at most
+  int runs, heads;
   size_t heads_bytes, sums_bytes, bytes;
-  Plan(int64_t t_total, int64_t n_seqs, bool one_each, int64_t n_heads, int dc, int64_t capacity) {
-    units = one_each ? n_seqs * ((n_heads + ROWS - 1) / ROWS) : t_total * n_heads / ROWS + n_seqs;
-    const int64_t tiles = units * ((capacity + KB - 1) / KB);
+  explicit Plan(const LatentAttendArgs& a) {
+    const int64_t T = a.pages.t_total, N = a.pages.n_seqs, H = a.n_heads;
+    rows = a.bf16 && T * H >= 64 * N ? 64 : 32;
+    const int tile = a.bf16 ? 64 : 32;
+    units = a.pages.cu ? T * H / rows + N : N * ((H + rows - 1) / rows);
+    const int64_t tiles = units * (((int64_t)a.pages.max_pages * a.pages.page_size + tile - 1) / tile);
     runs = (int)(tiles < RUNS ? (tiles < 1 ? 1 : tiles) : RUNS);
-    heads_bytes = ((size_t)units * sizeof(int2) + 255) / 256 * 256;
-    sums_bytes = (size_t)runs * 2 * ROWS * dc * 4;
-    bytes = heads_bytes + sums_bytes + (size_t)runs * 2 * ROWS * 8;
+    by_unit = units <= FEW_UNITS;
+    heads = by_unit ? (int)units : runs;
+    heads_bytes = ((size_t)heads * sizeof(int4) + 255) / 256 * 256;
+    sums_bytes = (size_t)runs * 2 * rows * a.dc * 4;
+    bytes = heads_bytes + sums_bytes + (size_t)runs * 2 * rows * 8;
   }
-  Plan(const LatentAttendArgs& a)
-      : Plan(a.pages.t_total, a.pages.n_seqs, !a.pages.cu, a.n_heads, a.dc,
-             (int64_t)a.pages.max_pages * a.pages.page_size) {}
 };
 
 struct Workspace {
-  int2* heads;   // per unit: the run of its first piece, and how many more follow (0: not cut)
-  float* sums;   // [2 runs][ROWS][dc]
-  float2* stats; // [2 runs][ROWS]: maximum (of scores), sum of weights (-1: nothing seen)
+  int4* heads;    // run of the unit's first piece, how many more follow (0: not cut), sequence, unit
+  float* sums;    // [2 runs][R][dc]
+  float2* stats;  // [2 runs][R]: maximum (of scores), sum of weights (-1: nothing seen)
+  int by_unit;
 };
 
 // What a call's sequence holds.
 struct Sequence {
   int start, tokens;        // first new token; new tokens
   int length, rows;         // seq_lens, and the rows of it that the table has places for
-  int64_t units;
-  int tiles;  // of each unit (one at least)
+  int64_t units;            // of R queries
+  int tiles;                // of KB rows, of each unit (one at least)
+  __device__ __forceinline__ int64_t all() const { return units * tiles; }
 };
+template <int R, int KB>
 __device__ __forceinline__ Sequence sequence_of(const LatentPages& g, int n_heads, int n) {
   Sequence s;
   s.start = seq_start(g.cu, n, g.t_total);
   s.tokens = max((g.cu ? seq_start(g.cu, n + 1, g.t_total) : n + 1) - s.start, 0);
   s.length = max(g.lens[n], 0);
   s.rows = min(s.length, g.max_pages * g.page_size);
-  s.units = ((int64_t)s.tokens * n_heads + ROWS - 1) / ROWS;
+  s.units = ((int64_t)s.tokens * n_heads + R - 1) / R;
   s.tiles = max((s.rows + KB - 1) / KB, 1);
   return s;
 }
@@ -83,41 +93,213 @@ __device__ __forceinline__ int64_t scan(int64_t x, int64_t* waves) {
   return x;
 }
 
-template <typename T, int DC, int DR>
+// How NW waves share a tile of KB cached rows and a unit of R queries.  Scores: KG
+// groups of keys times RG groups of queries, a wave NT tiles of 16 x 16.
+// Outputs: a wave COLS of the columns, NV x RV tiles of 32 x 32.
+template <typename T, int DC, int DR, int R>
 struct Shape {
   static constexpr int ES = sizeof(T), W = DC + DR;
+  static constexpr int KB = sizeof(T) == 2 ? 64 : 32;   // two tiles fill LDS
+  static constexpr int NW = sizeof(T) == 2 ? 8 : 4, THREADS = 64 * NW;
+  static constexpr int KG = KB / 16, RG = NW / KG, NT = R / (16 * RG);
+  static constexpr int COLS = DC / NW, NV = COLS / 32, RV = R / 32;
+  static constexpr int KS = W / 32;                     // slices of a score's sum
   static constexpr int blocks = (W * ES + 127) / 128;   // column blocks of a row
   static constexpr int tile = blocks * KB * 128;
   static constexpr int p_row = KB * ES + 16;            // bytes of a row of weights
 };
 
-template <typename T, int DC, int DR>
-__global__ __launch_bounds__(THREADS, 1) void latent_attend_kernel(LatentAttendArgs a, Workspace ws) {
-  using S = Shape<T, DC, DR>;
+// Source of the rows that do not exist.
+__device__ const uint4 kNoRow[8] = {};
+
+template <typename T, int DC, int DR, int R>
+struct Attend {
+  using S = Shape<T, DC, DR, R>;
   using F = typename Frag<T>::type;
-  constexpr int ES = S::ES, W = S::W, KS = W / 32, NV = DC / 128, NT = ROWS / 16;
-  __shared__ __attribute__((aligned(128))) char lds[S::tile];
-  __shared__ __attribute__((aligned(16))) char weights[ROWS * S::p_row];
-  __shared__ float tops[4][ROWS], sums[4][ROWS];
-  __shared__ int seen_by[4][ROWS], odd_by[4];
-  __shared__ int64_t waves[4], found[2];
+  using V4 = typename Vec4<T>::type;
+  static constexpr int ES = S::ES, KB = S::KB;
+
+  // LDS that the waves exchange through
+  struct Exchange {
+    float tops[S::KG][R], sums[S::KG][R];
+    int seen[S::KG][R], odd[S::NW];
+    uint64_t have[2][KB / 8];  // per tile in LDS: which of its rows exist, 8 bits to a row
+  };
+
+  F q[S::NT][S::KS];
+  f32x16 o[S::NV][S::RV];
+  int limit[S::NT], my_limit[S::RV];  // of the queries whose scores and outputs this lane holds
+  float top[S::NT], sum[S::NT], top_o[S::RV];
+  bool seen[S::NT];
+  RowFrags<T, KB, 32> key_frags;
+  ColFrags<T, KB> value_frags;
+
+  __device__ __forceinline__ Attend(int lane, int wave)
+      : key_frags(wave % S::KG * 16 + (lane & 15), lane >> 4), value_frags(S::COLS * wave, lane) {}
+
+  // One tile: positions j0 .. j0 + KB - 1, its rows in `tile`.
+  __device__ __forceinline__ void step(const char* tile, const uint64_t* have, char* weights, Exchange& x, int j0,
+                                       int least, float c, int lane, int wave) {
+    const int h = lane >> 5, col = lane & 15, grp = lane >> 4;
+    const int kg = wave % S::KG, rg = wave / S::KG;
+    const int key0 = kg * 16, row0 = rg * S::NT * 16;
+    f32x4 sc[S::NT], sd[S::NT];  // two sums each, so that products need not wait for one another
+#pragma unroll
+    for (int t = 0; t < S::NT; ++t) sc[t] = sd[t] = zero4();
+#pragma unroll
+    for (int s = 0; s < S::KS; ++s) {
+      const F key = key_frags.load(tile, s, 0);
+#pragma unroll
+      for (int t = 0; t < S::NT; ++t) (s % 2 ? sd : sc)[t] = mma32(key, q[t][s], (s % 2 ? sd : sc)[t]);
+    }
+#pragma unroll
+    for (int t = 0; t < S::NT; ++t) sc[t] += sd[t];
+    // element i of a lane: key0 + 4 grp + i.  All of a tile that every query sees
+    // whole is seen; else each (key, query) is looked at.
+    uint64_t all = ~(uint64_t)0;
+#pragma unroll
+    for (int g = 0; g < KB / 8; ++g) all &= have[g];
+    const bool whole = j0 + KB <= least && all == ~(uint64_t)0;
+    bool odd = false;  // a score that is not finite of a key that its query does not see
+    if (__builtin_expect(!whole, 0)) {
+      const int key = key0 + 4 * grp;
+      const uint32_t there = (uint32_t)(have[key >> 3] >> (8 * (key & 4)));
+#pragma unroll
+      for (int t = 0; t < S::NT; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const bool sees = j0 + key + i < limit[t] && (there >> (8 * i) & 1);
+          odd |= !sees && !__builtin_isfinite(sc[t][i]);
+          seen[t] |= sees;
+          sc[t][i] = sees ? sc[t][i] : -__builtin_inff();
+        }
+      odd = __any(odd);
+    } else {
+#pragma unroll
+      for (int t = 0; t < S::NT; ++t) seen[t] = true;
+    }
+#pragma unroll
+    for (int t = 0; t < S::NT; ++t) {
+      float m = -__builtin_inff();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) m = fmaxf(m, sc[t][i]);
+      m = fmaxf(m, __shfl_xor(m, 16));
+      m = fmaxf(m, __shfl_xor(m, 32));
+      if (grp == 0) x.tops[kg][row0 + 16 * t + col] = m;
+    }
+    if (lane == 0) x.odd[wave] = odd;
+    exchanged();
+    const auto tops_of = [&](int r, float m) {
+#pragma unroll
+      for (int k = 0; k < S::KG; ++k) m = fmaxf(m, x.tops[k][r]);
+      return m;
+    };
+#pragma unroll
+    for (int t = 0; t < S::NT; ++t) {
+      const float m = tops_of(row0 + 16 * t + col, top[t]);
+      // (a maximum's product with c is rounded the same way each time it is formed)
+      const float base = m == -__builtin_inff() ? 0.f : __fmul_rn(m, c);
+      sum[t] *= fast_exp2(__fmul_rn(top[t], c) - base);
+      top[t] = m;
+      V4 p;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float e = fast_exp2(sc[t][i] * c - base);
+        sum[t] += e;
+        p[i] = from_f32<T>(e);  // bf16: one rounding, 2^-8
+      }
+      *reinterpret_cast<V4*>(weights + (row0 + 16 * t + col) * S::p_row + (key0 + 4 * grp) * ES) = p;
+    }
+#pragma unroll
+    for (int v = 0; v < S::RV; ++v) {
+      const float m = tops_of(32 * v + (lane & 31), top_o[v]);
+      const float alpha = fast_exp2(__fmul_rn(top_o[v], c) - (m == -__builtin_inff() ? 0.f : __fmul_rn(m, c)));
+      top_o[v] = m;
+      if (__builtin_expect(__any(alpha != 1.f), 0)) {
+#pragma unroll
+        for (int d = 0; d < S::NV; ++d) o[d][v] *= alpha;
+      }
+    }
+    bool special = false;
+    if (__builtin_expect(!whole, 0)) {
+#pragma unroll
+      for (int w = 0; w < S::NW; ++w) special |= x.odd[w] != 0;
+    }
+    exchanged();
+
+    F p[S::RV][KB / 16];
+#pragma unroll
+    for (int v = 0; v < S::RV; ++v)
+#pragma unroll
+      for (int k = 0; k < KB / 16; ++k) {
+        const char* row = weights + (32 * v + (lane & 31)) * S::p_row + (16 * k + 4 * h) * ES;
+        const V4 lo = *reinterpret_cast<const V4*>(row), hi = *reinterpret_cast<const V4*>(row + 8 * ES);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) p[v][k][e] = lo[e], p[v][k][4 + e] = hi[e];
+      }
+    if (__builtin_expect(special, 0)) {
+      values_special(tile, p, j0, lane, wave);
+      return;
+    }
+#pragma unroll
+    for (int d = 0; d < S::NV; ++d)
+#pragma unroll
+      for (int k = 0; k < KB / 16; ++k) {
+        const F val = value_frags.load(tile, 16 * k, d);
+#pragma unroll
+        for (int v = 0; v < S::RV; ++v) o[d][v] = mma16(val, p[v][k], o[d][v]);
+      }
+  }
+
+  __device__ __forceinline__ void values_special(const char* tile, const F (&p)[S::RV][KB / 16], int j0, int lane,
+                                                 int wave) {
+    const int h = lane >> 5;
+#pragma unroll
+    for (int d = 0; d < S::NV; ++d)
+#pragma unroll
+      for (int v = 0; v < S::RV; ++v) {
+        f32x16 kinds = zero16();
+#pragma unroll
+        for (int k = 0; k < KB / 16; ++k) {
+          F val = value_frags.load(tile, 16 * k, d), kind, sees;
+          split_special(val, kind);
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            sees[e] = from_f32<T>(j0 + 16 * k + 8 * (e >> 2) + 4 * h + (e & 3) < my_limit[v] ? 1.f : 0.f);
+          o[d][v] = mma16(val, p[v][k], o[d][v]);
+          kinds = mma16(kind, sees, kinds);
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[d][v][i] = add_special(o[d][v][i], kinds[i]);
+      }
+  }
+};
+
+template <typename T, int DC, int DR, int R>
+__global__ __launch_bounds__((Shape<T, DC, DR, R>::THREADS), 1) void latent_attend_kernel(LatentAttendArgs a, Workspace ws) {
+  using S = Shape<T, DC, DR, R>;
+  using A = Attend<T, DC, DR, R>;
+  constexpr int ES = S::ES, W = S::W, KB = S::KB, THREADS = S::THREADS;
+  __shared__ __attribute__((aligned(128))) char even[S::tile];
+  __shared__ __attribute__((aligned(128))) char odd[S::tile];
+  __shared__ __attribute__((aligned(16))) char weights[R * S::p_row];
+  __shared__ typename A::Exchange x;
+  __shared__ int64_t waves[S::NW], found[2];
   const LatentPages& g = a.pages;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, h = lane >> 5;
   const int col = lane & 15, grp = lane >> 4;  // of a 16 x 16 tile
 
   // this workgroup's run of tiles, and the sequence it begins in
   const int run = blockIdx.x;
-  int64_t total = 0, mine = 0;
+  if (!ws.by_unit && threadIdx.x == 0) ws.heads[run].y = 0;
+  int64_t total = 0;
   for (int base = 0; base < g.n_seqs; base += THREADS) {
     const int n = base + threadIdx.x;
-    int64_t x = 0;
-    if (n < g.n_seqs) {
-      const Sequence s = sequence_of(g, a.n_heads, n);
-      x = s.units * s.tiles;
-    }
-    mine = scan(x, waves);
+    int64_t y = 0;
+    if (n < g.n_seqs) y = sequence_of<R, KB>(g, a.n_heads, n).all();
+    y = scan(y, waves);
     __syncthreads();
-    if (threadIdx.x == THREADS - 1) found[0] = mine;
+    if (threadIdx.x == THREADS - 1) found[0] = y;
     __syncthreads();
     total += found[0];
   }
@@ -129,15 +311,12 @@ __global__ __launch_bounds__(THREADS, 1) void latent_attend_kernel(LatentAttendA
   int64_t before = 0;
   for (int base = 0;; base += THREADS) {
     const int n = base + threadIdx.x;
-    int64_t x = 0;
-    if (n < g.n_seqs) {
-      const Sequence s = sequence_of(g, a.n_heads, n);
-      x = s.units * s.tiles;
-    }
-    const int64_t upto = before + scan(x, waves);
-    if (x > 0 && upto - x <= lo && lo < upto) {
+    int64_t y = 0;
+    if (n < g.n_seqs) y = sequence_of<R, KB>(g, a.n_heads, n).all();
+    const int64_t upto = before + scan(y, waves);
+    if (y > 0 && upto - y <= lo && lo < upto) {
       found[0] = n;
-      found[1] = upto - x;
+      found[1] = upto - y;
     }
     __syncthreads();
     if (threadIdx.x == THREADS - 1) waves[0] = upto;
@@ -150,281 +329,224 @@ __global__ __launch_bounds__(THREADS, 1) void latent_attend_kernel(LatentAttendA
   const float c = a.scale * kLog2e;
 
   for (int64_t pos = lo; pos < hi;) {
-    const Sequence s = sequence_of(g, a.n_heads, n);
+    const Sequence s = sequence_of<R, KB>(g, a.n_heads, n);
     const int64_t in_seq = pos - seq_at;
     const int unit = (int)(in_seq / s.tiles), tile0 = (int)(in_seq - (int64_t)unit * s.tiles);
     const int tile1 = (int)min((int64_t)s.tiles, tile0 + (hi - pos));
     const int64_t unit_at = pos - tile0;
     pos += tile1 - tile0;
     const int n_now = n;
-    if (pos - seq_at == s.units * s.tiles) {
+    if (pos - seq_at == s.all()) {
       seq_at = pos;
       ++n;
-      while (pos < hi && n + 1 < g.n_seqs && sequence_of(g, a.n_heads, n).units == 0) ++n;
+      while (pos < hi && n + 1 < g.n_seqs && sequence_of<R, KB>(g, a.n_heads, n).units == 0) ++n;
     }
 
     // the unit's queries: row r is head (r % H) of new token r / H; it sees positions
     // below limit(r)
-    const int row0 = unit * ROWS, n_rows = s.tokens * a.n_heads;
+    const int row0 = unit * R, n_rows = s.tokens * a.n_heads;
     const auto limit_of = [&](int r) {
       const int tok = min(row0 + r, n_rows - 1) / a.n_heads;
       return min(max(s.length + (tok + 1 - s.tokens), 0), s.rows);
     };
-    const int most = limit_of(ROWS - 1), least = limit_of(0);
-    F q[NT][KS];
-    int limit[NT];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const int r = min(row0 + 16 * t + col, n_rows - 1), tok = r / a.n_heads;
-      const T* qr = static_cast<const T*>(a.q) + (s.start + tok) * a.q_stride + (int64_t)(r - tok * a.n_heads) * W;
-      limit[t] = limit_of(16 * t + col);
-#pragma unroll
-      for (int k = 0; k < KS; ++k) q[t][k] = load_frag8<T>(qr + 32 * k + 8 * grp);
-    }
-    const int my_limit = limit_of(lane & 31);  // of the query whose output this lane holds
-    f32x16 o[NV];
-#pragma unroll
-    for (int d = 0; d < NV; ++d) o[d] = zero16();
-    float top[NT], sum[NT], top_o = -__builtin_inff();
-    bool seen[NT];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) top[t] = -__builtin_inff(), sum[t] = 0.f, seen[t] = false;
-
+    const int most = limit_of(R - 1), least = limit_of(0);
     const int tiles_end = min(tile1, (most + KB - 1) / KB);
-    for (int tile = tile0; tile < tiles_end; ++tile) {
-      // rows 16 wave .. 16 wave + 15 of the tile: eight lanes to a row's 128 bytes.  A
-      // position without a row is 0 and not seen.
-      const int j0 = tile * KB;
-      uint64_t have[2];
-      __syncthreads();
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const int row = 16 * wave + 8 * r + (lane >> 3), j = j0 + row, chunk = lane & 7;
-        int page = -1;
-        if (j < s.rows) page = g.table[(int64_t)n_now * g.max_pages + j / g.page_size];
-        const bool in = page >= 0 && page < g.n_pages;
-        have[r] = __ballot(in);
-        const char* src = static_cast<const char*>(a.cache) +
-                          ((int64_t)(in ? page : 0) * g.page_stride + (j % g.page_size) * g.row_stride) * ES + chunk * 16;
-#pragma unroll
-        for (int b = 0; b < S::blocks; ++b) {
-          uint4 x = {0, 0, 0, 0};
-          if (in && b * 128 + chunk * 16 < W * ES) x = *reinterpret_cast<const uint4*>(src + b * 128);
-          *reinterpret_cast<uint4*>(lds + b * KB * 128 + tile_at<KB>(row, chunk * 16)) = x;
-        }
-      }
-      __syncthreads();
 
-      // scores of this wave's keys: element i of a lane is key 4 grp + i
-      f32x4 x[NT];
+    // The next tile is fetched while one is worked on, and the pages of the one after
+    // that looked up.  A wave fetches eight rows, eight lanes to 128 bytes of a row, the
+    // chunks exchanged as tile_at has them; a position without a row is 0 and not seen.
+    static_assert(KB == 8 * S::NW, "a wave fetches eight rows of a tile");
+    const int fetch_row = 8 * wave + (lane >> 3), chunk = ((lane & 7) ^ (lane >> 3)) * 16;
+    int page = -1;
+    const auto look_up = [&](int tile) {
+      const int j = tile * KB + fetch_row;
+      page = -1;
+      if (tile < tiles_end && j < s.rows) page = g.table[(int64_t)n_now * g.max_pages + (uint32_t)j / (uint32_t)g.page_size];
+    };
+    const auto fetch = [&](int tile, char* to, uint64_t* have) {
+      const int j = tile * KB + fetch_row;
+      const bool in = page >= 0 && page < g.n_pages;
+      const uint64_t there = __ballot(in);
+      if (lane == 0) have[wave] = there;
+      const char* from = static_cast<const char*>(a.cache) +
+                         ((int64_t)page * g.page_stride + ((uint32_t)j % (uint32_t)g.page_size) * g.row_stride) * ES + chunk;
 #pragma unroll
-      for (int t = 0; t < NT; ++t) x[t] = zero4();
-#pragma unroll
-      for (int k = 0; k < KS; ++k) {
-        const F key = tile_row8<KB>(lds, 16 * wave + col, 32 * k + 8 * grp, T());
-#pragma unroll
-        for (int t = 0; t < NT; ++t) x[t] = mma32(key, q[t][k], x[t]);
+      for (int b = 0; b < S::blocks; ++b) {
+        const bool ok = in && 128 * b + chunk < W * ES;
+        fetch16(ok ? from + 128 * b : reinterpret_cast<const char*>(kNoRow) + chunk, to + (b * KB + 8 * wave) * 128);
       }
-      bool odd = false;  // a score that is not finite of a key that some query does not see
-      const uint64_t have_mine = grp < 2 ? have[0] : have[1];
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        float mx = -__builtin_inff();
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const bool sees = j0 + 16 * wave + 4 * grp + i < limit[t] && (have_mine >> (8 * (4 * (grp & 1) + i)) & 1);
-          odd |= !sees && !__builtin_isfinite(x[t][i]);
-          seen[t] |= sees;
-          if (!sees) x[t][i] = -__builtin_inff();
-          mx = fmaxf(mx, x[t][i]);
-        }
-        mx = fmaxf(mx, __shfl_xor(mx, 16));
-        mx = fmaxf(mx, __shfl_xor(mx, 32));
-        if (grp == 0) tops[wave][16 * t + col] = mx;
-      }
-      odd = __any(odd);
-      if (lane == 0) odd_by[wave] = odd;
-      __syncthreads();
-      const auto tops_of = [&](int r, float m) {
-        return fmaxf(m, fmaxf(fmaxf(tops[0][r], tops[1][r]), fmaxf(tops[2][r], tops[3][r])));
-      };
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        const float m = tops_of(16 * t + col, top[t]);
-        const float base = m == -__builtin_inff() ? 0.f : __fmul_rn(m, c);
-        sum[t] *= fast_exp2(__fmul_rn(top[t], c) - base);
-        top[t] = m;
-        typename Vec4<T>::type p;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float e = fast_exp2(x[t][i] * c - base);
-          sum[t] += e;
-          p[i] = from_f32<T>(e);  // bf16: one rounding, 2^-8
-        }
-        *reinterpret_cast<typename Vec4<T>::type*>(weights + (16 * t + col) * S::p_row + (16 * wave + 4 * grp) * ES) = p;
-      }
-      const float m = tops_of(lane & 31, top_o);
-      const float alpha = fast_exp2(__fmul_rn(top_o, c) - (m == -__builtin_inff() ? 0.f : __fmul_rn(m, c)));
-      top_o = m;
-      if (__any(alpha != 1.f)) {
-#pragma unroll
-        for (int d = 0; d < NV; ++d) o[d] *= alpha;
-      }
-      const bool special = j0 + KB > least && (odd_by[0] | odd_by[1] | odd_by[2] | odd_by[3]);
-      __syncthreads();
+      look_up(tile + 1);
+    };
 
-      // O^T of this wave's columns
-      F p[4];
+    A s_(lane, wave);
+    look_up(tile0);
+    __syncthreads();  // LDS of the piece before is done with
+    if (tile0 < tiles_end) fetch(tile0, even, x.have[0]);
+    const int kg = wave % S::KG, rg = wave / S::KG;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const char* row = weights + (lane & 31) * S::p_row + (16 * k + 4 * h) * ES;
-        const auto lo4 = *reinterpret_cast<const typename Vec4<T>::type*>(row);
-        const auto hi4 = *reinterpret_cast<const typename Vec4<T>::type*>(row + 8 * ES);
+    for (int t = 0; t < S::NT; ++t) {
+      const int r = min(row0 + (rg * S::NT + t) * 16 + col, n_rows - 1), tok = r / a.n_heads;
+      const T* qr = static_cast<const T*>(a.q) + (s.start + tok) * a.q_stride + (int64_t)(r - tok * a.n_heads) * W;
+      s_.limit[t] = limit_of((rg * S::NT + t) * 16 + col);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) p[k][e] = lo4[e], p[k][4 + e] = hi4[e];
-      }
-      if (!special) {
+      for (int k = 0; k < S::KS; ++k) s_.q[t][k] = load_frag8<T>(qr + 32 * k + 8 * grp);
+      s_.top[t] = -__builtin_inff(), s_.sum[t] = 0.f, s_.seen[t] = false;
+    }
 #pragma unroll
-        for (int d = 0; d < NV; ++d)
+    for (int v = 0; v < S::RV; ++v) {
+      s_.my_limit[v] = limit_of(32 * v + (lane & 31));
+      s_.top_o[v] = -__builtin_inff();
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            o[d] = mma16(tile_col8<KB>(lds, 16 * k, (DC / 4) * wave + 32 * d, lane, T()), p[k], o[d]);
-      } else {
-#pragma unroll
-        for (int d = 0; d < NV; ++d) {
-          f32x16 kinds = zero16();
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            F v = tile_col8<KB>(lds, 16 * k, (DC / 4) * wave + 32 * d, lane, T()), kind, sees;
-            split_special(v, kind);
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              sees[e] = from_f32<T>(j0 + 16 * k + 8 * (e >> 2) + 4 * h + (e & 3) < my_limit ? 1.f : 0.f);
-            o[d] = mma16(v, p[k], o[d]);
-            kinds = mma16(kind, sees, kinds);
-          }
-#pragma unroll
-          for (int i = 0; i < 16; ++i) o[d][i] = add_special(o[d][i], kinds[i]);
-        }
-      }
+      for (int d = 0; d < S::NV; ++d) s_.o[d][v] = zero16();
+    }
+    for (int tile = tile0; tile < tiles_end; tile += 2) {
+      fetched();
+      if (tile + 1 < tiles_end) fetch(tile + 1, odd, x.have[1]);
+      s_.step(even, x.have[0], weights, x, tile * KB, least, c, lane, wave);
+      if (tile + 1 == tiles_end) break;
+      fetched();
+      if (tile + 2 < tiles_end) fetch(tile + 2, even, x.have[0]);
+      s_.step(odd, x.have[1], weights, x, (tile + 1) * KB, least, c, lane, wave);
     }
 
     // the sum of weights of each row, over lanes and waves
     __syncthreads();
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      float x = sum[t];
-      x += __shfl_xor(x, 16);
-      x += __shfl_xor(x, 32);
-      int any = seen[t];
+    for (int t = 0; t < S::NT; ++t) {
+      float y = s_.sum[t];
+      y += __shfl_xor(y, 16);
+      y += __shfl_xor(y, 32);
+      int any = s_.seen[t];
       any |= __shfl_xor(any, 16);
       any |= __shfl_xor(any, 32);
-      if (grp == 0) sums[wave][16 * t + col] = x, seen_by[wave][16 * t + col] = any;
+      const int r = (rg * S::NT + t) * 16 + col;
+      if (grp == 0) x.sums[kg][r] = y, x.seen[kg][r] = any;
     }
     __syncthreads();
-    const int r = lane & 31;
-    const float all = (sums[0][r] + sums[1][r]) + (sums[2][r] + sums[3][r]);
-    const bool some = seen_by[0][r] | seen_by[1][r] | seen_by[2][r] | seen_by[3][r];
-    if (tile0 == 0) {
+    if (tile0 == 0 && threadIdx.x == 0) {
       // the unit's last piece is in the last run that begins before the unit ends
       const int more = (int)(((unit_at + s.tiles) * runs + total - 1) / total) - 1 - run;
-      if (threadIdx.x == 0) {
-        const int64_t id = g.cu ? first_block<ROWS>(s.start, a.n_heads, n_now) : (int64_t)n_now * s.units;
-        ws.heads[id + unit] = int2{run, more};
-      }
+      const int64_t id = g.cu ? first_block<R>(s.start, a.n_heads, n_now) : (int64_t)n_now * s.units;
+      if (ws.by_unit || more > 0) ws.heads[ws.by_unit ? id + unit : run] = int4{run, more, n_now, unit};
     }
-    if (tile0 == 0 && tile1 == s.tiles) {
-      if (row0 + r < n_rows) {
+#pragma unroll
+    for (int v = 0; v < S::RV; ++v) {
+      const int r = 32 * v + (lane & 31);
+      float all = 0.f;
+      int some = 0;
+#pragma unroll
+      for (int k = 0; k < S::KG; ++k) all += x.sums[k][r], some |= x.seen[k][r];
+      if (tile0 == 0 && tile1 == s.tiles) {
+        if (row0 + r >= n_rows) continue;
         const int tok = (row0 + r) / a.n_heads;
         const float inv = some ? 1.f / all : 0.f;  // no key: O is 0
         T* out = static_cast<T*>(a.o) + (s.start + tok) * a.o_stride + (int64_t)(row0 + r - tok * a.n_heads) * DC +
-                 (DC / 4) * wave;
+                 S::COLS * wave;
 #pragma unroll
-        for (int d = 0; d < NV; ++d)
+        for (int d = 0; d < S::NV; ++d)
 #pragma unroll
           for (int b = 0; b < 4; ++b) {
             typename Vec4<T>::type y;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) y[e] = from_f32<T>(o[d][4 * b + e] * inv);
+            for (int e = 0; e < 4; ++e) y[e] = from_f32<T>(s_.o[d][v][4 * b + e] * inv);
             *reinterpret_cast<typename Vec4<T>::type*>(out + 32 * d + 8 * b + 4 * h) = y;
           }
+      } else {
+        const int64_t place = 2 * (int64_t)run + (tile0 == 0 ? 1 : 0);
+        float* out = ws.sums + (place * R + r) * DC + S::COLS * wave;
+#pragma unroll
+        for (int d = 0; d < S::NV; ++d)
+#pragma unroll
+          for (int b = 0; b < 4; ++b)
+            *reinterpret_cast<f32x4*>(out + 32 * d + 8 * b + 4 * h) =
+                f32x4{s_.o[d][v][4 * b], s_.o[d][v][4 * b + 1], s_.o[d][v][4 * b + 2], s_.o[d][v][4 * b + 3]};
+        if (wave == 0 && lane < 32) ws.stats[place * R + r] = float2{s_.top_o[v], some ? all : -1.f};
       }
-    } else {
-      const int64_t place = 2 * (int64_t)run + (tile0 == 0 ? 1 : 0);
-      float* out = ws.sums + (place * ROWS + r) * DC + (DC / 4) * wave;
-#pragma unroll
-      for (int d = 0; d < NV; ++d)
-#pragma unroll
-        for (int b = 0; b < 4; ++b)
-          *reinterpret_cast<f32x4*>(out + 32 * d + 8 * b + 4 * h) =
-              f32x4{o[d][4 * b], o[d][4 * b + 1], o[d][4 * b + 2], o[d][4 * b + 3]};
-      if (wave == 0 && lane < 32) ws.stats[place * ROWS + r] = float2{top_o, some ? all : -1.f};
     }
   }
 }
 
-// A row of a unit that was cut: the pieces' sums, each at its own maximum, brought to
-// the largest.  A thread takes four columns.
-template <typename T, int DC>
-__global__ __launch_bounds__(DC / 4) void latent_join_kernel(LatentAttendArgs a, Workspace ws) {
+// The rows of units that were cut: the pieces' sums, each at its own maximum, brought
+// to the largest.  A workgroup takes 128 columns of a row at a time, eight groups of 32
+// threads every eighth piece each; `shares` workgroups share a unit.
+template <typename T, int DC, int R, int KB>
+__global__ __launch_bounds__(JOIN_THREADS) void latent_join_kernel(LatentAttendArgs a, Workspace ws, int shares) {
+  constexpr int PARTS = DC / 128, GROUPS = 8;
+  __shared__ float factors[RUNS], wide[GROUPS][128];
+  __shared__ float tops[4], sums[4];
+  __shared__ int some_by[4];
   const LatentPages& g = a.pages;
-  const int64_t id = blockIdx.x / ROWS;
-  const int r = blockIdx.x % ROWS;
-  int n;
-  int64_t unit;
-  if (g.cu) {
-    n = find_sequence<ROWS>(g.cu, g.n_seqs, g.t_total, a.n_heads, id);
-    unit = id - first_block<ROWS>(seq_start(g.cu, n, g.t_total), a.n_heads, n);
-  } else {
-    const int64_t per = (a.n_heads + ROWS - 1) / ROWS;
-    n = (int)(id / per);
-    unit = id - n * per;
+  const int id = blockIdx.x / shares;
+  if (ws.by_unit && g.cu) {  // a number may be no unit's, and its head then was not written
+    const int n = find_sequence<R>(g.cu, g.n_seqs, g.t_total, a.n_heads, id);
+    const Sequence s = sequence_of<R, KB>(g, a.n_heads, n);
+    const int64_t unit = id - first_block<R>(s.start, a.n_heads, n);
+    if (unit < 0 || unit >= s.units) return;
   }
-  const Sequence s = sequence_of(g, a.n_heads, n);
-  if (unit < 0 || unit >= s.units) return;
-  const int64_t row = unit * ROWS + r;
-  if (row >= (int64_t)s.tokens * a.n_heads) return;
-  const int2 head = ws.heads[id];
-  if (head.y == 0) return;
+  const int4 head = ws.heads[id];
+  const int more = head.y;
+  if (more == 0) return;
+  const Sequence s = sequence_of<R, KB>(g, a.n_heads, head.z);
+  const int row0 = head.w * R, n_rows = s.tokens * a.n_heads;
   const float c = a.scale * kLog2e;
-  const auto place = [&](int i) { return ((int64_t)(i == 0 ? 2 * head.x + 1 : 2 * (head.x + i)) * ROWS + r); };
-  float top = -__builtin_inff();
-  for (int i = 0; i <= head.y; ++i) {
-    const float2 st = ws.stats[place(i)];
-    if (!(st.y == -1.f)) top = fmaxf(top, st.x);
-  }
-  const float base = top == -__builtin_inff() ? 0.f : __fmul_rn(top, c);
-  f32x4 o = zero4();
-  float sum = 0.f;
-  bool some = false;
-  for (int i = 0; i <= head.y; ++i) {
-    const float2 st = ws.stats[place(i)];
-    if (st.y == -1.f) continue;
-    some = true;
-    const float f = fast_exp2(__fmul_rn(st.x, c) - base);
-    sum += f * st.y;
-    o += f * *reinterpret_cast<const f32x4*>(ws.sums + place(i) * DC + 4 * threadIdx.x);
-  }
-  const float inv = some ? 1.f / sum : 0.f;
-  const int tok = (int)(row / a.n_heads);
-  T* out = static_cast<T*>(a.o) + (s.start + tok) * a.o_stride + (row - (int64_t)tok * a.n_heads) * DC + 4 * threadIdx.x;
-  typename Vec4<T>::type y;
+  const int i = threadIdx.x, lane = i & 63, wave = i >> 6;
+  const int group = i / 32, at = 4 * (i & 31);
+  for (int item = blockIdx.x % shares; item < R * PARTS; item += shares) {
+    const int part = item % PARTS, r = item / PARTS;
+    if (row0 + r >= n_rows) return;
+    const auto place = [&](int k) { return ((int64_t)(k == 0 ? 2 * head.x + 1 : 2 * (head.x + k)) * R + r); };
+    // a piece each thread: at most RUNS of them
+    const float2 st = i <= more ? ws.stats[place(i)] : float2{0.f, -1.f};
+    const bool mine = !(st.y == -1.f);
+    float top = mine ? st.x : -__builtin_inff();
 #pragma unroll
-  for (int e = 0; e < 4; ++e) y[e] = from_f32<T>(o[e] * inv);
-  *reinterpret_cast<typename Vec4<T>::type*>(out) = y;
+    for (int d = 32; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
+    __syncthreads();
+    if (lane == 0) tops[wave] = top;
+    __syncthreads();
+    top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+    const float base = top == -__builtin_inff() ? 0.f : __fmul_rn(top, c);
+    const float f = mine ? fast_exp2(__fmul_rn(st.x, c) - base) : 0.f;
+    factors[i] = f;
+    float sum = mine ? f * st.y : 0.f;
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d);
+    const bool any = __any(mine);
+    if (lane == 0) sums[wave] = sum, some_by[wave] = any;
+    __syncthreads();
+    f32x4 o = zero4();
+#pragma unroll 4
+    for (int k = group; k <= more; k += GROUPS)
+      o += factors[k] * *reinterpret_cast<const f32x4*>(ws.sums + place(k) * DC + 128 * part + at);
+    *reinterpret_cast<f32x4*>(&wide[group][at]) = o;
+    __syncthreads();
+    if (i < 128) {
+      float y = 0.f;
+#pragma unroll
+      for (int k = 0; k < GROUPS; ++k) y += wide[k][i];
+      sum = (sums[0] + sums[1]) + (sums[2] + sums[3]);
+      const float inv = some_by[0] | some_by[1] | some_by[2] | some_by[3] ? 1.f / sum : 0.f;
+      const int tok = (row0 + r) / a.n_heads;
+      static_cast<T*>(a.o)[(s.start + tok) * a.o_stride + (int64_t)(row0 + r - tok * a.n_heads) * DC + 128 * part + i] =
+          from_f32<T>(y * inv);
+    }
+  }
 }
 
-template <typename T, int DC, int DR>
+template <typename T, int DC, int DR, int R>
 hipError_t run(const LatentAttendArgs& a, const Plan& plan, const Workspace& ws, hipStream_t stream) {
-  hipError_t e = enqueue(latent_attend_kernel<T, DC, DR>, (unsigned)plan.runs, THREADS, stream, a, ws);
+  hipError_t e = enqueue(latent_attend_kernel<T, DC, DR, R>, (unsigned)plan.runs, Shape<T, DC, DR, R>::THREADS, stream, a, ws);
   if (e != hipSuccess) return e;
-  return enqueue(latent_join_kernel<T, DC>, (unsigned)(plan.units * ROWS), DC / 4, stream, a, ws);
+  const int shares = plan.by_unit ? R * (DC / 128) : 16;
+  return enqueue(latent_join_kernel<T, DC, R, Shape<T, DC, DR, R>::KB>, (unsigned)(plan.heads * shares), JOIN_THREADS, stream,
+                 a, ws, shares);
 }
 
-template <typename T>
+template <typename T, int R>
 hipError_t by_shape(const LatentAttendArgs& a, const Plan& plan, const Workspace& ws, hipStream_t stream) {
-  if (a.dc == 512) return a.dr == 64 ? run<T, 512, 64>(a, plan, ws, stream) : run<T, 512, 32>(a, plan, ws, stream);
-  return a.dr == 64 ? run<T, 256, 64>(a, plan, ws, stream) : run<T, 256, 32>(a, plan, ws, stream);
+  if (a.dc == 512)
+    return a.dr == 64 ? run<T, 512, 64, R>(a, plan, ws, stream) : run<T, 512, 32, R>(a, plan, ws, stream);
+  return a.dr == 64 ? run<T, 256, 64, R>(a, plan, ws, stream) : run<T, 256, 32, R>(a, plan, ws, stream);
 }
 
 }  // namespace
@@ -437,9 +559,10 @@ hipError_t launch_latent_attend(const LatentAttendArgs& a, void* workspace, hipS
   if (a.pages.t_total == 0 || a.pages.n_seqs == 0) return hipSuccess;
   const Plan plan(a);
   char* w = static_cast<char*>(workspace);
-  const Workspace ws = {reinterpret_cast<int2*>(w), reinterpret_cast<float*>(w + plan.heads_bytes),
-                        reinterpret_cast<float2*>(w + plan.heads_bytes + plan.sums_bytes)};
-  return a.bf16 ? by_shape<bf16>(a, plan, ws, stream) : by_shape<float>(a, plan, ws, stream);
+  const Workspace ws = {reinterpret_cast<int4*>(w), reinterpret_cast<float*>(w + plan.heads_bytes),
+                        reinterpret_cast<float2*>(w + plan.heads_bytes + plan.sums_bytes), plan.by_unit};
+  if (!a.bf16) return by_shape<float, 32>(a, plan, ws, stream);
+  return plan.rows == 64 ? by_shape<bf16, 64>(a, plan, ws, stream) : by_shape<bf16, 32>(a, plan, ws, stream);
 }
 
 }  // namespace kda

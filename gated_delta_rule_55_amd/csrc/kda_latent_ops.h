@@ -50,44 +50,78 @@ __device__ __forceinline__ int tile_at(int row, int byte) {
   return (byte >> 7) * (ROWS * 128) + row * 128 + ((((byte >> 4) & 7) ^ (row & 7)) << 4) + (byte & 15);
 }
 
-// Columns c .. c + 7 of a row, as a fragment (c a multiple of 8).
-template <int ROWS>
-__device__ __forceinline__ bf16x8 tile_row8(const char* t, int row, int c, bf16) {
-  return *reinterpret_cast<const bf16x8*>(t + tile_at<ROWS>(row, 2 * c));
-}
-template <int ROWS>
-__device__ __forceinline__ f32x8 tile_row8(const char* t, int row, int c, float) {
-  const f32x4 lo = *reinterpret_cast<const f32x4*>(t + tile_at<ROWS>(row, 4 * c));
-  const f32x4 hi = *reinterpret_cast<const f32x4*>(t + tile_at<ROWS>(row, 4 * c + 16));
-  return f32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+// A value that the compiler keeps in a register as it is: an address that constants
+// are added to (they go into the instructions) instead of one address for each.
+__device__ __forceinline__ int kept(int x) {
+  asm("" : "+v"(x));
+  return x;
 }
 
-// The transposed fragment: column c0 + l % 32 of the 16 rows from row0, in the
-// keys' order.  bf16: two transposing reads, in each of which 16 lanes fetch four
-// rows' 16 columns (lane i four of row i / 4) and lane i receives column i of
-// the four.
+// Fragments of a tile's rows: columns 8 x .. 8 x + 7 of every slice of STEP columns,
+// for the lane's row and x.
+template <typename T, int ROWS, int STEP>
+struct RowFrags {
+  static constexpr int N = 128 / (STEP * sizeof(T)), HALVES = sizeof(T) / 2;
+  int at[N][HALVES];
+  __device__ __forceinline__ RowFrags(int row, int x) {
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+      for (int f = 0; f < HALVES; ++f) at[n][f] = kept(tile_at<ROWS>(row, (STEP * n + 8 * x) * (int)sizeof(T) + 16 * f));
+  }
+  // slice s, `below` rows (a multiple of 8) below the lane's
+  __device__ __forceinline__ typename Frag<T>::type load(const char* tile, int s, int below) const {
+    const char* p = tile + (s / N) * (ROWS * 128) + below * 128;
+    typename Frag<T>::type f;
+    if constexpr (HALVES == 1) {
+      f = *reinterpret_cast<const bf16x8*>(p + at[s % N][0]);
+    } else {
+      const f32x4 lo = *reinterpret_cast<const f32x4*>(p + at[s % N][0]);
+      const f32x4 hi = *reinterpret_cast<const f32x4*>(p + at[s % N][1]);
+      f = f32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+    }
+    return f;
+  }
+};
+
+// Transposed fragments: column c0 + 32 d + lane % 32 of 16 rows, in the keys' order (c0
+// a multiple of 64, or of 32 where d is 0).  bf16: two transposing reads, in each of
+// which 16 lanes fetch four rows' 16 columns (lane i four of row i / 4) and lane i
+// receives column i of the four.
 __device__ __forceinline__ s16x4 read_tr(const char* p) {
   typedef __attribute__((address_space(3))) s16x4* lds;
   return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds)p);
 }
-template <int ROWS>
-__device__ __forceinline__ bf16x8 tile_col8(const char* t, int row0, int c0, int lane, bf16) {
-  const int row = row0 + 4 * (lane >> 5) + ((lane & 15) >> 2);
-  const int byte = 2 * (c0 + 16 * ((lane >> 4) & 1) + 4 * (lane & 3));
-  const s16x4 lo = read_tr(t + tile_at<ROWS>(row, byte));
-  const s16x4 hi = read_tr(t + tile_at<ROWS>(row + 8, byte));
-  typedef short s16x8 __attribute__((ext_vector_type(8)));
-  return __builtin_bit_cast(bf16x8, s16x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]});
-}
-template <int ROWS>
-__device__ __forceinline__ f32x8 tile_col8(const char* t, int row0, int c0, int lane, float) {
-  const int h = lane >> 5, byte = 4 * (c0 + (lane & 31));
-  f32x8 f;
+template <typename T, int ROWS>
+struct ColFrags {
+  static constexpr int N = sizeof(T) == 2 ? 2 : 4;
+  int at[N];
+  __device__ __forceinline__ ColFrags(int c0, int lane) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e)
-    f[e] = *reinterpret_cast<const float*>(t + tile_at<ROWS>(row0 + 8 * (e >> 2) + 4 * h + (e & 3), byte));
-  return f;
-}
+    for (int n = 0; n < N; ++n) {
+      if constexpr (sizeof(T) == 2)
+        at[n] = tile_at<ROWS>(4 * (lane >> 5) + ((lane & 15) >> 2), 2 * (c0 + 32 * n + 16 * ((lane >> 4) & 1) + 4 * (lane & 3)));
+      else
+        at[n] = tile_at<ROWS>(4 * (lane >> 5) + n, 4 * (c0 + (lane & 31)));
+      at[n] = kept(at[n]);
+    }
+  }
+  // the 16 rows from row0 (a multiple of 16)
+  __device__ __forceinline__ typename Frag<T>::type load(const char* tile, int row0, int d) const {
+    typename Frag<T>::type f;
+    if constexpr (sizeof(T) == 2) {
+      const char* p = tile + (d / 2) * (ROWS * 128) + row0 * 128 + at[d % 2];
+      const s16x4 lo = read_tr(p), hi = read_tr(p + 8 * 128);
+      typedef short s16x8 __attribute__((ext_vector_type(8)));
+      f = __builtin_bit_cast(bf16x8, s16x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]});
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        f[e] = *reinterpret_cast<const float*>(tile + d * (ROWS * 128) + (row0 + 8 * (e >> 2)) * 128 + at[e & 3]);
+    }
+    return f;
+  }
+};
 
 // Values that are not finite, in rows that some of a tile's queries see and
 // others do not: a weight of 0 would turn them into NaN for all.  They are taken
@@ -99,19 +133,19 @@ __device__ __forceinline__ void split_special(F& v, F& kind) {
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     const float x = (float)v[e];
-    const bool finite = __builtin_isfinite(x);
-    kind[e] = finite ? 0.f : (x != x ? 1048576.f : (x > 0.f ? 1.f : 1024.f));
-    if (!finite) v[e] = 0.f;
+    const uint32_t bits = __builtin_bit_cast(uint32_t, x);
+    const bool finite = (bits & 0x7f800000u) != 0x7f800000u;
+    const float which = (bits & 0x7fffffu) ? 1048576.f : (bits >> 31) ? 1024.f : 1.f;
+    kind[e] = finite ? 0.f : which;
+    v[e] = finite ? x : 0.f;
   }
 }
 __device__ __forceinline__ float add_special(float acc, float kinds) {
-  if (kinds == 0.f) return acc;
   const float inf = __builtin_inff();
-  if (kinds >= 1048576.f) return __builtin_nanf("");
-  const bool neg = kinds >= 1024.f;
+  const bool nan = kinds >= 1048576.f, neg = kinds >= 1024.f;
   const bool pos = kinds != 1024.f * __builtin_floorf(kinds * (1.f / 1024.f));
-  if (pos) acc += inf;
-  if (neg) acc -= inf;
+  acc += pos || nan ? inf : 0.f;
+  acc -= neg ? inf : 0.f;  // both kinds, and NaN's own: inf - inf
   return acc;
 }
 
@@ -125,7 +159,21 @@ __device__ __forceinline__ void fetch16(__amdgpu_buffer_rsrc_t r, int place, int
   typedef __attribute__((address_space(3))) void* lds;
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds)at, 16, place, uniform, 0, 0);
 }
-// Waits for this wave's fetches and LDS accesses, then for the workgroup's other waves.
+// The same from a pointer of each lane's own.
+__device__ __forceinline__ void fetch16(const char* from, char* at) {
+  typedef __attribute__((address_space(3))) void* lds;
+  typedef const __attribute__((address_space(1))) void* global;
+  __builtin_amdgcn_global_load_lds((global)from, (lds)at, 16, 0, 0);
+}
+// Waits for this wave's LDS accesses, then for the workgroup's other waves.  (Fetches
+// stay under way, which __syncthreads would wait for.)
+__device__ __forceinline__ void exchanged() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0)
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+// The same, and for this wave's fetches.
 __device__ __forceinline__ void fetched() {
   asm volatile("" ::: "memory");
   __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)

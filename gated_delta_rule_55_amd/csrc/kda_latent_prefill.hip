@@ -33,6 +33,14 @@ struct Prefill {
   F q[KS];
   f32x16 o[NV];
   float m, l;
+  RowFrags<T, KB, 16> key_frags;
+  ColFrags<T, KB> value_frags;
+
+  __device__ __forceinline__ explicit Prefill(int lane)
+      : m(-__builtin_inff()), l(0.f), key_frags(lane & 31, lane >> 5), value_frags(0, lane) {
+#pragma unroll
+    for (int d = 0; d < NV; ++d) o[d] = zero16();
+  }
 
   // One tile's keys from position `key0` on, of which this lane's query sees those
   // up to `last`.  MASKED: some query of the wave does not see all of them.
@@ -44,9 +52,8 @@ struct Prefill {
     for (int k = 0; k < KS; ++k)
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        const int row = 32 * t + (lane & 31), col = 16 * k + 8 * h;
-        s[t] = mma16(16 * k < DN ? tile_row8<KB>(lds, row, col, T()) : tile_row8<KB>(lds + L::pe, row, col - DN, T()),
-                     q[k], s[t]);
+        const F key = 16 * k < DN ? key_frags.load(lds, k, 32 * t) : key_frags.load(lds + L::pe, k - DN / 16, 32 * t);
+        s[t] = mma16(key, q[k], s[t]);
       }
     if (MASKED) {
 #pragma unroll
@@ -76,19 +83,19 @@ struct Prefill {
         p[2 * t + (i >> 3)][i & 7] = from_f32<T>(x);  // bf16: one rounding, 2^-8
       }
     l = l * alpha + sum;
-    if (__any(alpha != 1.f)) {
+    if (__builtin_expect(__any(alpha != 1.f), 0)) {
 #pragma unroll
       for (int d = 0; d < NV; ++d) o[d] *= alpha;
     }
     const char* values = lds + L::v;
-    if (MASKED && special(values, lane)) {
+    if (MASKED && __builtin_expect(special(values, lane), 0)) {
       values_special(values, p, key0, last, lane);
       return;
     }
 #pragma unroll
     for (int d = 0; d < NV; ++d)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) o[d] = mma16(tile_col8<KB>(values, 16 * k, 32 * d, lane, T()), p[k], o[d]);
+      for (int k = 0; k < 4; ++k) o[d] = mma16(value_frags.load(values, 16 * k, d), p[k], o[d]);
   }
 
   // Whether a tile holds a value that is not finite.
@@ -115,7 +122,7 @@ struct Prefill {
       f32x16 kinds = zero16();
 #pragma unroll 1
       for (int k = 0; k < 4; ++k) {
-        F v = tile_col8<KB>(values, 16 * k, 32 * d, lane, T()), kind, sees, w;
+        F v = value_frags.load(values, 16 * k, d), kind, sees, w;
         split_special(v, kind);
 #pragma unroll
         for (int e = 0; e < 8; ++e)
@@ -160,17 +167,13 @@ __global__ __launch_bounds__(THREADS, sizeof(T) == 2 ? 2 : 1) void latent_prefil
   // keys that the workgroup's last query sees
   const int end = min(first + QB, queries) + (keys - queries);
 
-  P s;
+  P s(lane);
   {
     const char* row = static_cast<const char*>(a.q) +
                       ((int64_t)(q0 + min(mine, queries - 1)) * a.q_stride + (int64_t)head * (DN + DR) + 8 * h) * ES;
 #pragma unroll
     for (int k = 0; k < P::KS; ++k) s.q[k] = load_frag8<T>(reinterpret_cast<const T*>(row + 16 * k * ES));
   }
-#pragma unroll
-  for (int d = 0; d < P::NV; ++d) s.o[d] = zero16();
-  s.m = -__builtin_inff();
-  s.l = 0.f;
 
   // The next tile is fetched while one is worked on.  A wave fetches 16 rows of it,
   // eight lanes to 128 bytes of a row, the chunks exchanged as tile_at has them.
@@ -203,7 +206,7 @@ __global__ __launch_bounds__(THREADS, sizeof(T) == 2 ? 2 : 1) void latent_prefil
     }
   };
   auto work = [&](int t, const char* tile) {
-    if (t * KB + KB - 1 <= wave_last)
+    if (__builtin_expect(t * KB + KB - 1 <= wave_last, 1))
       s.template step<false>(tile, t * KB, last, c, lane);
     else if (t * KB <= wave_last + 31)
       s.template step<true>(tile, t * KB, last, c, lane);

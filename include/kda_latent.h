@@ -104,7 +104,7 @@ typedef struct {
   int32_t max_pages;           /* >= 1: columns of block_table                  */
   int32_t n_pages;             /* >= 0                                          */
   float scale;                 /* > 0                                           */
-  int64_t t_total;             /* new tokens; (t_total H) / 32 + N < 2^23       */
+  int64_t t_total;             /* new tokens; t_total H <= 2^31 - 65            */
   const void* q;
   const void* cache;
   void* o;
