@@ -81,6 +81,9 @@ int check_pages(int32_t dtype, int32_t n_seqs, int32_t dc, int32_t dr, int32_t p
   if (g->page_stride > ((int64_t)1 << 40)) return KDA_ERR_SHAPE;
   if (n_pages > 0 && g->page_stride > ((int64_t)1 << 60) / n_pages) return KDA_ERR_SHAPE;
   g->page_size = page_size;
+  g->page_shift = 31;
+  while (((int64_t)1 << (g->page_shift - 31)) < page_size) ++g->page_shift;
+  g->page_factor = (uint32_t)((((uint64_t)1 << g->page_shift) + page_size - 1) / page_size);
   g->max_pages = max_pages;
   g->n_pages = n_pages;
   g->n_seqs = n_seqs;

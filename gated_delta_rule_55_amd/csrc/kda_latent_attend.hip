@@ -94,14 +94,14 @@ __device__ __forceinline__ int64_t scan(int64_t x, int64_t* waves) {
 }
 
 // How NW waves share a tile of KB cached rows and a unit of R queries.  Scores: KG
-// groups of keys times RG groups of queries, a wave NT tiles of 16 x 16.
+// groups of keys times RG groups of queries, a wave KT tiles of 16 x 16.
 // Outputs: a wave COLS of the columns, NV x RV tiles of 32 x 32.
 template <typename T, int DC, int DR, int R>
 struct Shape {
   static constexpr int ES = sizeof(T), W = DC + DR;
   static constexpr int KB = sizeof(T) == 2 ? 64 : 32;   // two tiles fill LDS
   static constexpr int NW = sizeof(T) == 2 ? 8 : 4, THREADS = 64 * NW;
-  static constexpr int KG = KB / 16, RG = NW / KG, NT = R / (16 * RG);
+  static constexpr int RG = R / 16, KG = NW / RG, KT = KB / (16 * KG);
   static constexpr int COLS = DC / NW, NV = COLS / 32, RV = R / 32;
   static constexpr int KS = W / 32;                     // slices of a score's sum
   static constexpr int blocks = (W * ES + 127) / 128;   // column blocks of a row
@@ -109,8 +109,8 @@ struct Shape {
   static constexpr int p_row = KB * ES + 16;            // bytes of a row of weights
 };
 
-// Source of the rows that do not exist.
-__device__ const uint4 kNoRow[8] = {};
+// Source of the rows that do not exist: as long as the longest row.
+__device__ const uint4 kNoRow[(512 + 64) * 4 / 16] = {};
 
 template <typename T, int DC, int DR, int R>
 struct Attend {
@@ -126,89 +126,104 @@ struct Attend {
     uint64_t have[2][KB / 8];  // per tile in LDS: which of its rows exist, 8 bits to a row
   };
 
-  F q[S::NT][S::KS];
+  F q[S::KS];
   f32x16 o[S::NV][S::RV];
-  int limit[S::NT], my_limit[S::RV];  // of the queries whose scores and outputs this lane holds
-  float top[S::NT], sum[S::NT], top_o[S::RV];
-  bool seen[S::NT];
+  int limit, my_limit[S::RV];  // of the queries whose scores and outputs this lane holds
+  float top, sum, top_o[S::RV];
+  bool seen;
   RowFrags<T, KB, 32> key_frags;
   ColFrags<T, KB> value_frags;
 
   __device__ __forceinline__ Attend(int lane, int wave)
-      : key_frags(wave % S::KG * 16 + (lane & 15), lane >> 4), value_frags(S::COLS * wave, lane) {}
-
-  // One tile: positions j0 .. j0 + KB - 1, its rows in `tile`.
-  __device__ __forceinline__ void step(const char* tile, const uint64_t* have, char* weights, Exchange& x, int j0,
-                                       int least, float c, int lane, int wave) {
-    const int h = lane >> 5, col = lane & 15, grp = lane >> 4;
-    const int kg = wave % S::KG, rg = wave / S::KG;
-    const int key0 = kg * 16, row0 = rg * S::NT * 16;
-    f32x4 sc[S::NT], sd[S::NT];  // two sums each, so that products need not wait for one another
+      : top(-__builtin_inff()), sum(0.f), seen(false), key_frags(wave % S::KG * S::KT * 16 + (lane & 15), lane >> 4),
+        value_frags(S::COLS * wave, lane) {
 #pragma unroll
-    for (int t = 0; t < S::NT; ++t) sc[t] = sd[t] = zero4();
+    for (int v = 0; v < S::RV; ++v) {
+      top_o[v] = -__builtin_inff();
 #pragma unroll
-    for (int s = 0; s < S::KS; ++s) {
-      const F key = key_frags.load(tile, s, 0);
-#pragma unroll
-      for (int t = 0; t < S::NT; ++t) (s % 2 ? sd : sc)[t] = mma32(key, q[t][s], (s % 2 ? sd : sc)[t]);
+      for (int d = 0; d < S::NV; ++d) o[d][v] = zero16();
     }
-#pragma unroll
-    for (int t = 0; t < S::NT; ++t) sc[t] += sd[t];
-    // element i of a lane: key0 + 4 grp + i.  All of a tile that every query sees
-    // whole is seen; else each (key, query) is looked at.
+  }
+
+  // Whether every query of the unit sees all of the tile at j0.
+  static __device__ __forceinline__ bool whole(const uint64_t* have, int j0, int least) {
     uint64_t all = ~(uint64_t)0;
 #pragma unroll
     for (int g = 0; g < KB / 8; ++g) all &= have[g];
-    const bool whole = j0 + KB <= least && all == ~(uint64_t)0;
-    bool odd = false;  // a score that is not finite of a key that its query does not see
-    if (__builtin_expect(!whole, 0)) {
-      const int key = key0 + 4 * grp;
-      const uint32_t there = (uint32_t)(have[key >> 3] >> (8 * (key & 4)));
+    return j0 + KB <= least && all == ~(uint64_t)0;
+  }
+
+  // One tile: positions j0 .. j0 + KB - 1, its rows in `tile`.  Where not all of it is seen
+  // each (key, query) is looked at, and false is returned if a key that is not seen holds
+  // a value that is not finite (its score is not): SAFE then does the whole unit again.
+  template <bool SAFE>
+  __device__ __forceinline__ bool step(const char* tile, const uint64_t* have, char* weights, Exchange& x, int j0,
+                                       int least, float c, int lane, int wave) {
+    const bool not_whole = !whole(have, j0, least);
+    const int h = lane >> 5, col = lane & 15, grp = lane >> 4;
+    const int kg = wave % S::KG, rg = wave / S::KG;
+    const int key0 = kg * S::KT * 16, row = rg * 16 + col;
+    f32x4 sc[S::KT], sd[S::KT];  // two sums each, so that products need not wait for one another
 #pragma unroll
-      for (int t = 0; t < S::NT; ++t)
+    for (int k = 0; k < S::KT; ++k) sc[k] = sd[k] = zero4();
+    pipelined<F, S::KS * S::KT, 4>([&](int i) { return key_frags.load(tile, i / S::KT, 16 * (i % S::KT)); },
+                                   [&](int i, F key) {
+                                     f32x4& acc = i / S::KT % 2 ? sd[i % S::KT] : sc[i % S::KT];
+                                     acc = mma32(key, q[i / S::KT], acc);
+                                   });
+#pragma unroll
+    for (int k = 0; k < S::KT; ++k) sc[k] += sd[k];
+    // element i of a lane: key key0 + 16 k + 4 grp + i
+    bool odd = false;  // a score that is not finite of a key that its query does not see
+    if (__builtin_expect(not_whole, 0)) {
+#pragma unroll
+      for (int k = 0; k < S::KT; ++k) {
+        const int key = key0 + 16 * k + 4 * grp;
+        const uint32_t there = (uint32_t)(have[key >> 3] >> (8 * (key & 4)));
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const bool sees = j0 + key + i < limit[t] && (there >> (8 * i) & 1);
-          odd |= !sees && !__builtin_isfinite(sc[t][i]);
-          seen[t] |= sees;
-          sc[t][i] = sees ? sc[t][i] : -__builtin_inff();
+          const bool sees = j0 + key + i < limit && (there >> (8 * i) & 1);
+          odd |= !sees && !__builtin_isfinite(sc[k][i]);
+          seen |= sees;
+          sc[k][i] = sees ? sc[k][i] : -__builtin_inff();
         }
+      }
       odd = __any(odd);
     } else {
-#pragma unroll
-      for (int t = 0; t < S::NT; ++t) seen[t] = true;
+      seen = true;
     }
+    float mx = -__builtin_inff();
 #pragma unroll
-    for (int t = 0; t < S::NT; ++t) {
-      float m = -__builtin_inff();
+    for (int k = 0; k < S::KT; ++k)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) m = fmaxf(m, sc[t][i]);
-      m = fmaxf(m, __shfl_xor(m, 16));
-      m = fmaxf(m, __shfl_xor(m, 32));
-      if (grp == 0) x.tops[kg][row0 + 16 * t + col] = m;
-    }
-    if (lane == 0) x.odd[wave] = odd;
+      for (int i = 0; i < 4; ++i) mx = fmaxf(mx, sc[k][i]);
+    mx = fmaxf(mx, __shfl_xor(mx, 16));
+    mx = fmaxf(mx, __shfl_xor(mx, 32));
+    if (grp == 0) x.tops[kg][row] = mx;
+    if (!SAFE && lane == 0) x.odd[wave] = odd;
     exchanged();
     const auto tops_of = [&](int r, float m) {
 #pragma unroll
       for (int k = 0; k < S::KG; ++k) m = fmaxf(m, x.tops[k][r]);
       return m;
     };
-#pragma unroll
-    for (int t = 0; t < S::NT; ++t) {
-      const float m = tops_of(row0 + 16 * t + col, top[t]);
+    {
+      const float m = tops_of(row, top);
       // (a maximum's product with c is rounded the same way each time it is formed)
       const float base = m == -__builtin_inff() ? 0.f : __fmul_rn(m, c);
-      sum[t] *= fast_exp2(__fmul_rn(top[t], c) - base);
-      top[t] = m;
-      V4 p;
+      sum *= fast_exp2(__fmul_rn(top, c) - base);
+      top = m;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float e = fast_exp2(sc[t][i] * c - base);
-        sum[t] += e;
-        p[i] = from_f32<T>(e);  // bf16: one rounding, 2^-8
+      for (int k = 0; k < S::KT; ++k) {
+        V4 p;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float e = fast_exp2(sc[k][i] * c - base);
+          sum += e;
+          p[i] = from_f32<T>(e);  // bf16: one rounding, 2^-8
+        }
+        *reinterpret_cast<V4*>(weights + row * S::p_row + (key0 + 16 * k + 4 * grp) * ES) = p;
       }
-      *reinterpret_cast<V4*>(weights + (row0 + 16 * t + col) * S::p_row + (key0 + 4 * grp) * ES) = p;
     }
 #pragma unroll
     for (int v = 0; v < S::RV; ++v) {
@@ -220,39 +235,44 @@ struct Attend {
         for (int d = 0; d < S::NV; ++d) o[d][v] *= alpha;
       }
     }
-    bool special = false;
-    if (__builtin_expect(!whole, 0)) {
+    if (!SAFE && __builtin_expect(not_whole, 0)) {
 #pragma unroll
-      for (int w = 0; w < S::NW; ++w) special |= x.odd[w] != 0;
+      for (int w = 0; w < S::NW; ++w) odd |= x.odd[w] != 0;
+      if (odd) return false;
     }
     exchanged();
 
-    F p[S::RV][KB / 16];
+    const auto weight = [&](int v, int k) {
+      const char* from = weights + (32 * v + (lane & 31)) * S::p_row + (16 * k + 4 * h) * ES;
+      const V4 lo = *reinterpret_cast<const V4*>(from), hi = *reinterpret_cast<const V4*>(from + 8 * ES);
+      F p;
 #pragma unroll
-    for (int v = 0; v < S::RV; ++v)
-#pragma unroll
-      for (int k = 0; k < KB / 16; ++k) {
-        const char* row = weights + (32 * v + (lane & 31)) * S::p_row + (16 * k + 4 * h) * ES;
-        const V4 lo = *reinterpret_cast<const V4*>(row), hi = *reinterpret_cast<const V4*>(row + 8 * ES);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) p[v][k][e] = lo[e], p[v][k][4 + e] = hi[e];
-      }
-    if (__builtin_expect(special, 0)) {
-      values_special(tile, p, j0, lane, wave);
-      return;
+      for (int e = 0; e < 4; ++e) p[e] = lo[e], p[4 + e] = hi[e];
+      return p;
+    };
+    if (SAFE && not_whole) {
+      values_special(tile, weight, j0, lane);
+      return true;
     }
+    // step k NV + d: columns 32 d, rows 16 k of the tile, and their weights with d = 0
+    F p[2][S::RV];
 #pragma unroll
-    for (int d = 0; d < S::NV; ++d)
+    for (int v = 0; v < S::RV; ++v) p[0][v] = weight(v, 0);
+    pipelined<F, KB / 16 * S::NV, 2>([&](int i) { return value_frags.load(tile, 16 * (i / S::NV), i % S::NV); },
+                                     [&](int i, F val) {
+                                       const int k = i / S::NV, d = i % S::NV;
+                                       if (d == 0 && k + 1 < KB / 16) {
 #pragma unroll
-      for (int k = 0; k < KB / 16; ++k) {
-        const F val = value_frags.load(tile, 16 * k, d);
+                                         for (int v = 0; v < S::RV; ++v) p[(k + 1) % 2][v] = weight(v, k + 1);
+                                       }
 #pragma unroll
-        for (int v = 0; v < S::RV; ++v) o[d][v] = mma16(val, p[v][k], o[d][v]);
-      }
+                                       for (int v = 0; v < S::RV; ++v) o[d][v] = mma16(val, p[k % 2][v], o[d][v]);
+                                     });
+    return true;
   }
 
-  __device__ __forceinline__ void values_special(const char* tile, const F (&p)[S::RV][KB / 16], int j0, int lane,
-                                                 int wave) {
+  template <typename Weight>
+  __device__ __forceinline__ void values_special(const char* tile, Weight weight, int j0, int lane) {
     const int h = lane >> 5;
 #pragma unroll
     for (int d = 0; d < S::NV; ++d)
@@ -266,7 +286,7 @@ struct Attend {
 #pragma unroll
           for (int e = 0; e < 8; ++e)
             sees[e] = from_f32<T>(j0 + 16 * k + 8 * (e >> 2) + 4 * h + (e & 3) < my_limit[v] ? 1.f : 0.f);
-          o[d][v] = mma16(val, p[v][k], o[d][v]);
+          o[d][v] = mma16(val, weight(v, k), o[d][v]);
           kinds = mma16(kind, sees, kinds);
         }
 #pragma unroll
@@ -275,19 +295,155 @@ struct Attend {
   }
 };
 
+// What a workgroup does of a unit: tiles tile0 .. tile1 - 1 of it.
+struct Piece {
+  int n, unit, tile0, tile1;
+  int64_t unit_at;  // where the unit's tiles begin, of all tiles of the call
+  int run, runs;
+  int64_t total;
+};
+
+template <typename T, int DC, int DR, int R, bool SAFE>
+__device__ __forceinline__ bool attend_piece(const LatentAttendArgs& a, const Workspace& ws, const Sequence& s,
+                                             const Piece& pc, char* even, char* odd, char* weights,
+                                             typename Attend<T, DC, DR, R>::Exchange& x) {
+  using S = Shape<T, DC, DR, R>;
+  using A = Attend<T, DC, DR, R>;
+  constexpr int ES = S::ES, W = S::W, KB = S::KB;
+  const LatentPages& g = a.pages;
+  const int lane = threadIdx.x & 63, wave = wave_index(), h = lane >> 5;
+  const int col = lane & 15, grp = lane >> 4;  // of a 16 x 16 tile
+  const float c = a.scale * kLog2e;
+  const int unit = pc.unit, tile0 = pc.tile0, tile1 = pc.tile1, n_now = pc.n, run = pc.run;
+  // the unit's queries: row r is head (r % H) of new token r / H; it sees positions
+  // below limit(r)
+  const int row0 = unit * R, n_rows = s.tokens * a.n_heads;
+  const auto limit_of = [&](int r) {
+    const int tok = min(row0 + r, n_rows - 1) / a.n_heads;
+    return min(max(s.length + (tok + 1 - s.tokens), 0), s.rows);
+  };
+  const int most = limit_of(R - 1), least = limit_of(0);
+  const int tiles_end = min(tile1, (most + KB - 1) / KB);
+
+  // The next tile is fetched while one is worked on, and the pages of the one after
+  // that looked up.  A wave fetches eight rows, eight lanes to 128 bytes of a row, the
+  // chunks exchanged as tile_at has them; a position without a row is 0 and not seen.
+  static_assert(KB == 8 * S::NW, "a wave fetches eight rows of a tile");
+  const int fetch_row = 8 * wave + (lane >> 3), chunk = ((lane & 7) ^ (lane >> 3)) * 16;
+  int page = -1;
+  const auto look_up = [&](int tile) {
+    const int j = tile * KB + fetch_row;
+    page = -1;
+    if (tile < tiles_end && j < s.rows) page = g.table[(int64_t)n_now * g.max_pages + page_of(g, j)];
+  };
+  const auto fetch = [&](int tile, char* to, uint64_t* have) {
+    const int j = tile * KB + fetch_row;
+    const bool in = page >= 0 && page < g.n_pages;
+    const uint64_t there = __ballot(in);
+    if (lane == 0) have[wave] = there;
+    const char* from = reinterpret_cast<const char*>(kNoRow) + chunk;
+    if (in)
+      from = static_cast<const char*>(a.cache) +
+             ((int64_t)page * g.page_stride + row_in_page(g, j, page_of(g, j)) * g.row_stride) * ES + chunk;
+#pragma unroll
+    for (int b = 0; b < S::blocks; ++b) {
+      const char* p = from + 128 * b;
+      if (128 * (b + 1) > W * ES && 128 * b + chunk >= W * ES) p = reinterpret_cast<const char*>(kNoRow);
+      fetch16(p, to + (b * KB + 8 * wave) * 128);
+    }
+    look_up(tile + 1);
+  };
+
+  A s_(lane, wave);
+  look_up(tile0);
+  __syncthreads();  // LDS of the piece before is done with
+  if (tile0 < tiles_end) fetch(tile0, even, x.have[0]);
+  const int kg = wave % S::KG, rg = wave / S::KG;
+  {
+    const int r = min(row0 + rg * 16 + col, n_rows - 1), tok = r / a.n_heads;
+    const T* qr = static_cast<const T*>(a.q) + (s.start + tok) * a.q_stride + (int64_t)(r - tok * a.n_heads) * W;
+    s_.limit = limit_of(rg * 16 + col);
+#pragma unroll
+    for (int k = 0; k < S::KS; ++k) s_.q[k] = load_frag8<T>(qr + 32 * k + 8 * grp);
+  }
+#pragma unroll
+  for (int v = 0; v < S::RV; ++v) s_.my_limit[v] = limit_of(32 * v + (lane & 31));
+  for (int tile = tile0; tile < tiles_end; tile += 2) {
+    fetched();
+    if (tile + 1 < tiles_end) fetch(tile + 1, odd, x.have[1]);
+    if (!s_.template step<SAFE>(even, x.have[0], weights, x, tile * KB, least, c, lane, wave)) return false;
+    if (tile + 1 == tiles_end) break;
+    fetched();
+    if (tile + 2 < tiles_end) fetch(tile + 2, even, x.have[0]);
+    if (!s_.template step<SAFE>(odd, x.have[1], weights, x, (tile + 1) * KB, least, c, lane, wave)) return false;
+  }
+
+  // the sum of weights of each row, over lanes and waves
+  __syncthreads();
+  {
+    float y = s_.sum;
+    y += __shfl_xor(y, 16);
+    y += __shfl_xor(y, 32);
+    int any = s_.seen;
+    any |= __shfl_xor(any, 16);
+    any |= __shfl_xor(any, 32);
+    if (grp == 0) x.sums[kg][rg * 16 + col] = y, x.seen[kg][rg * 16 + col] = any;
+  }
+  __syncthreads();
+  if (tile0 == 0 && threadIdx.x == 0) {
+    // the unit's last piece is in the last run that begins before the unit ends
+    const int more = (int)(((pc.unit_at + s.tiles) * pc.runs + pc.total - 1) / pc.total) - 1 - run;
+    const int64_t id = g.cu ? first_block<R>(s.start, a.n_heads, n_now) : (int64_t)n_now * s.units;
+    if (ws.by_unit || more > 0) ws.heads[ws.by_unit ? id + unit : run] = int4{run, more, n_now, unit};
+  }
+#pragma unroll
+  for (int v = 0; v < S::RV; ++v) {
+    const int r = 32 * v + (lane & 31);
+    float all = 0.f;
+    int some = 0;
+#pragma unroll
+    for (int k = 0; k < S::KG; ++k) all += x.sums[k][r], some |= x.seen[k][r];
+    if (tile0 == 0 && tile1 == s.tiles) {
+      if (row0 + r >= n_rows) continue;
+      const int tok = (row0 + r) / a.n_heads;
+      const float inv = some ? 1.f / all : 0.f;  // no key: O is 0
+      T* out = static_cast<T*>(a.o) + (s.start + tok) * a.o_stride + (int64_t)(row0 + r - tok * a.n_heads) * DC +
+               S::COLS * wave;
+#pragma unroll
+      for (int d = 0; d < S::NV; ++d)
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          typename Vec4<T>::type y;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) y[e] = from_f32<T>(s_.o[d][v][4 * b + e] * inv);
+          *reinterpret_cast<typename Vec4<T>::type*>(out + 32 * d + 8 * b + 4 * h) = y;
+        }
+    } else {
+      const int64_t place = 2 * (int64_t)run + (tile0 == 0 ? 1 : 0);
+      float* out = ws.sums + (place * R + r) * DC + S::COLS * wave;
+#pragma unroll
+      for (int d = 0; d < S::NV; ++d)
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+          *reinterpret_cast<f32x4*>(out + 32 * d + 8 * b + 4 * h) =
+              f32x4{s_.o[d][v][4 * b], s_.o[d][v][4 * b + 1], s_.o[d][v][4 * b + 2], s_.o[d][v][4 * b + 3]};
+      if (wave == 0 && lane < 32) ws.stats[place * R + r] = float2{s_.top_o[v], some ? all : -1.f};
+    }
+  }
+  return true;
+}
+
 template <typename T, int DC, int DR, int R>
 __global__ __launch_bounds__((Shape<T, DC, DR, R>::THREADS), 1) void latent_attend_kernel(LatentAttendArgs a, Workspace ws) {
   using S = Shape<T, DC, DR, R>;
   using A = Attend<T, DC, DR, R>;
-  constexpr int ES = S::ES, W = S::W, KB = S::KB, THREADS = S::THREADS;
+  constexpr int KB = S::KB, THREADS = S::THREADS;
   __shared__ __attribute__((aligned(128))) char even[S::tile];
   __shared__ __attribute__((aligned(128))) char odd[S::tile];
   __shared__ __attribute__((aligned(16))) char weights[R * S::p_row];
   __shared__ typename A::Exchange x;
   __shared__ int64_t waves[S::NW], found[2];
   const LatentPages& g = a.pages;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, h = lane >> 5;
-  const int col = lane & 15, grp = lane >> 4;  // of a 16 x 16 tile
 
   // this workgroup's run of tiles, and the sequence it begins in
   const int run = blockIdx.x;
@@ -326,7 +482,6 @@ __global__ __launch_bounds__((Shape<T, DC, DR, R>::THREADS), 1) void latent_atte
   }
   int n = (int)found[0];
   int64_t seq_at = found[1];  // the tile that the sequence's first unit begins with
-  const float c = a.scale * kLog2e;
 
   for (int64_t pos = lo; pos < hi;) {
     const Sequence s = sequence_of<R, KB>(g, a.n_heads, n);
@@ -342,127 +497,9 @@ __global__ __launch_bounds__((Shape<T, DC, DR, R>::THREADS), 1) void latent_atte
       while (pos < hi && n + 1 < g.n_seqs && sequence_of<R, KB>(g, a.n_heads, n).units == 0) ++n;
     }
 
-    // the unit's queries: row r is head (r % H) of new token r / H; it sees positions
-    // below limit(r)
-    const int row0 = unit * R, n_rows = s.tokens * a.n_heads;
-    const auto limit_of = [&](int r) {
-      const int tok = min(row0 + r, n_rows - 1) / a.n_heads;
-      return min(max(s.length + (tok + 1 - s.tokens), 0), s.rows);
-    };
-    const int most = limit_of(R - 1), least = limit_of(0);
-    const int tiles_end = min(tile1, (most + KB - 1) / KB);
-
-    // The next tile is fetched while one is worked on, and the pages of the one after
-    // that looked up.  A wave fetches eight rows, eight lanes to 128 bytes of a row, the
-    // chunks exchanged as tile_at has them; a position without a row is 0 and not seen.
-    static_assert(KB == 8 * S::NW, "a wave fetches eight rows of a tile");
-    const int fetch_row = 8 * wave + (lane >> 3), chunk = ((lane & 7) ^ (lane >> 3)) * 16;
-    int page = -1;
-    const auto look_up = [&](int tile) {
-      const int j = tile * KB + fetch_row;
-      page = -1;
-      if (tile < tiles_end && j < s.rows) page = g.table[(int64_t)n_now * g.max_pages + (uint32_t)j / (uint32_t)g.page_size];
-    };
-    const auto fetch = [&](int tile, char* to, uint64_t* have) {
-      const int j = tile * KB + fetch_row;
-      const bool in = page >= 0 && page < g.n_pages;
-      const uint64_t there = __ballot(in);
-      if (lane == 0) have[wave] = there;
-      const char* from = static_cast<const char*>(a.cache) +
-                         ((int64_t)page * g.page_stride + ((uint32_t)j % (uint32_t)g.page_size) * g.row_stride) * ES + chunk;
-#pragma unroll
-      for (int b = 0; b < S::blocks; ++b) {
-        const bool ok = in && 128 * b + chunk < W * ES;
-        fetch16(ok ? from + 128 * b : reinterpret_cast<const char*>(kNoRow) + chunk, to + (b * KB + 8 * wave) * 128);
-      }
-      look_up(tile + 1);
-    };
-
-    A s_(lane, wave);
-    look_up(tile0);
-    __syncthreads();  // LDS of the piece before is done with
-    if (tile0 < tiles_end) fetch(tile0, even, x.have[0]);
-    const int kg = wave % S::KG, rg = wave / S::KG;
-#pragma unroll
-    for (int t = 0; t < S::NT; ++t) {
-      const int r = min(row0 + (rg * S::NT + t) * 16 + col, n_rows - 1), tok = r / a.n_heads;
-      const T* qr = static_cast<const T*>(a.q) + (s.start + tok) * a.q_stride + (int64_t)(r - tok * a.n_heads) * W;
-      s_.limit[t] = limit_of((rg * S::NT + t) * 16 + col);
-#pragma unroll
-      for (int k = 0; k < S::KS; ++k) s_.q[t][k] = load_frag8<T>(qr + 32 * k + 8 * grp);
-      s_.top[t] = -__builtin_inff(), s_.sum[t] = 0.f, s_.seen[t] = false;
-    }
-#pragma unroll
-    for (int v = 0; v < S::RV; ++v) {
-      s_.my_limit[v] = limit_of(32 * v + (lane & 31));
-      s_.top_o[v] = -__builtin_inff();
-#pragma unroll
-      for (int d = 0; d < S::NV; ++d) s_.o[d][v] = zero16();
-    }
-    for (int tile = tile0; tile < tiles_end; tile += 2) {
-      fetched();
-      if (tile + 1 < tiles_end) fetch(tile + 1, odd, x.have[1]);
-      s_.step(even, x.have[0], weights, x, tile * KB, least, c, lane, wave);
-      if (tile + 1 == tiles_end) break;
-      fetched();
-      if (tile + 2 < tiles_end) fetch(tile + 2, even, x.have[0]);
-      s_.step(odd, x.have[1], weights, x, (tile + 1) * KB, least, c, lane, wave);
-    }
-
-    // the sum of weights of each row, over lanes and waves
-    __syncthreads();
-#pragma unroll
-    for (int t = 0; t < S::NT; ++t) {
-      float y = s_.sum[t];
-      y += __shfl_xor(y, 16);
-      y += __shfl_xor(y, 32);
-      int any = s_.seen[t];
-      any |= __shfl_xor(any, 16);
-      any |= __shfl_xor(any, 32);
-      const int r = (rg * S::NT + t) * 16 + col;
-      if (grp == 0) x.sums[kg][r] = y, x.seen[kg][r] = any;
-    }
-    __syncthreads();
-    if (tile0 == 0 && threadIdx.x == 0) {
-      // the unit's last piece is in the last run that begins before the unit ends
-      const int more = (int)(((unit_at + s.tiles) * runs + total - 1) / total) - 1 - run;
-      const int64_t id = g.cu ? first_block<R>(s.start, a.n_heads, n_now) : (int64_t)n_now * s.units;
-      if (ws.by_unit || more > 0) ws.heads[ws.by_unit ? id + unit : run] = int4{run, more, n_now, unit};
-    }
-#pragma unroll
-    for (int v = 0; v < S::RV; ++v) {
-      const int r = 32 * v + (lane & 31);
-      float all = 0.f;
-      int some = 0;
-#pragma unroll
-      for (int k = 0; k < S::KG; ++k) all += x.sums[k][r], some |= x.seen[k][r];
-      if (tile0 == 0 && tile1 == s.tiles) {
-        if (row0 + r >= n_rows) continue;
-        const int tok = (row0 + r) / a.n_heads;
-        const float inv = some ? 1.f / all : 0.f;  // no key: O is 0
-        T* out = static_cast<T*>(a.o) + (s.start + tok) * a.o_stride + (int64_t)(row0 + r - tok * a.n_heads) * DC +
-                 S::COLS * wave;
-#pragma unroll
-        for (int d = 0; d < S::NV; ++d)
-#pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            typename Vec4<T>::type y;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) y[e] = from_f32<T>(s_.o[d][v][4 * b + e] * inv);
-            *reinterpret_cast<typename Vec4<T>::type*>(out + 32 * d + 8 * b + 4 * h) = y;
-          }
-      } else {
-        const int64_t place = 2 * (int64_t)run + (tile0 == 0 ? 1 : 0);
-        float* out = ws.sums + (place * R + r) * DC + S::COLS * wave;
-#pragma unroll
-        for (int d = 0; d < S::NV; ++d)
-#pragma unroll
-          for (int b = 0; b < 4; ++b)
-            *reinterpret_cast<f32x4*>(out + 32 * d + 8 * b + 4 * h) =
-                f32x4{s_.o[d][v][4 * b], s_.o[d][v][4 * b + 1], s_.o[d][v][4 * b + 2], s_.o[d][v][4 * b + 3]};
-        if (wave == 0 && lane < 32) ws.stats[place * R + r] = float2{s_.top_o[v], some ? all : -1.f};
-      }
-    }
+    const Piece pc = {n_now, unit, tile0, tile1, unit_at, run, runs, total};
+    if (!attend_piece<T, DC, DR, R, false>(a, ws, s, pc, even, odd, weights, x))
+      attend_piece<T, DC, DR, R, true>(a, ws, s, pc, even, odd, weights, x);
   }
 }
 

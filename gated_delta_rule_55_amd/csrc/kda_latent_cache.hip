@@ -84,9 +84,9 @@ __global__ __launch_bounds__(64 * APPEND_TOKENS) void latent_append_kernel(Laten
   }
   T* row[2] = {a.rows ? static_cast<T*>(a.rows) + t * a.rows_stride : nullptr, nullptr};
   if (at >= 0 && at < (int64_t)g.max_pages * g.page_size) {
-    const int page = g.table[(int64_t)n * g.max_pages + at / g.page_size];
+    const int place = page_of(g, (int)at), page = g.table[(int64_t)n * g.max_pages + place];
     if (page >= 0 && page < g.n_pages)
-      row[1] = static_cast<T*>(a.cache) + page * g.page_stride + (at % g.page_size) * g.row_stride;
+      row[1] = static_cast<T*>(a.cache) + page * g.page_stride + row_in_page(g, (int)at, place) * g.row_stride;
   }
 #pragma unroll
   for (int w = 0; w < 2; ++w) {

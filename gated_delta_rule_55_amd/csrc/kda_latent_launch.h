@@ -24,6 +24,8 @@ struct LatentPrefillArgs {
 // The tables of a paged cache.
 struct LatentPages {
   int page_size, max_pages, n_pages;
+  uint32_t page_factor;  // j / page_size = j page_factor >> page_shift for 0 <= j < 2^31:
+  int page_shift;        // ceil(2^shift / size), shift = 31 + ceil(log2 size)
   int64_t page_stride, row_stride;
   const int32_t* table;
   const int32_t* lens;

@@ -14,6 +14,7 @@
 #pragma once
 
 #include "kda_device.h"
+#include "kda_latent_launch.h"
 
 namespace kda {
 
@@ -106,11 +107,12 @@ struct ColFrags {
       at[n] = kept(at[n]);
     }
   }
-  // the 16 rows from row0 (a multiple of 16)
+  // the 16 rows from row0 (a multiple of 16); d may be a variable (no register is indexed)
   __device__ __forceinline__ typename Frag<T>::type load(const char* tile, int row0, int d) const {
     typename Frag<T>::type f;
     if constexpr (sizeof(T) == 2) {
-      const char* p = tile + (d / 2) * (ROWS * 128) + row0 * 128 + at[d % 2];
+      const int first = at[0], second = at[1];
+      const char* p = tile + (d / 2) * (ROWS * 128) + row0 * 128 + (d % 2 ? second : first);
       const s16x4 lo = read_tr(p), hi = read_tr(p + 8 * 128);
       typedef short s16x8 __attribute__((ext_vector_type(8)));
       f = __builtin_bit_cast(bf16x8, s16x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]});
@@ -122,6 +124,30 @@ struct ColFrags {
     return f;
   }
 };
+
+// N matrix steps whose operands come from LDS, in groups of G: a group's operands are
+// read while the group before runs.  (Left to itself the compiler reads each operand
+// right before its step, where registers are short.)  load(i) answers step i's operand
+// and step(i, operand) runs it.
+template <typename F, int N, int G, typename Load, typename Step>
+__device__ __forceinline__ void pipelined(Load load, Step step) {
+  F now[G], next[G];
+#pragma unroll
+  for (int i = 0; i < G; ++i) now[i] = load(i);
+#pragma unroll
+  for (int g = 0; g < N; g += G) {
+#pragma unroll
+    for (int i = 0; i < G; ++i)
+      if (g + G + i < N) next[i] = load(g + G + i);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < G; ++i)
+      if (g + i < N) step(g + i, now[i]);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < G; ++i) now[i] = next[i];
+  }
+}
 
 // Values that are not finite, in rows that some of a tile's queries see and
 // others do not: a weight of 0 would turn them into NaN for all.  They are taken
@@ -183,6 +209,15 @@ __device__ __forceinline__ void fetched() {
 
 // Values of the other half of the wave (lane l ^ 32).
 __device__ __forceinline__ float other_half(float x) { return __shfl_xor(x, 32); }
+
+// The wave of this thread in its workgroup, as a scalar.
+__device__ __forceinline__ int wave_index() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
+
+// The page of position j of a sequence (0 <= j < 2^31), and j's row there.
+__device__ __forceinline__ int page_of(const LatentPages& g, int j) {
+  return (int)((uint64_t)(uint32_t)j * g.page_factor >> g.page_shift);
+}
+__device__ __forceinline__ int row_in_page(const LatentPages& g, int j, int page) { return j - page * g.page_size; }
 
 // cu[n], or n where there is no table (one token each), clamped to [0, total].
 __device__ __forceinline__ int seq_start(const int32_t* cu, int n, int total) {

@@ -33,28 +33,29 @@ struct Prefill {
   F q[KS];
   f32x16 o[NV];
   float m, l;
+  bool special;
   RowFrags<T, KB, 16> key_frags;
   ColFrags<T, KB> value_frags;
 
   __device__ __forceinline__ explicit Prefill(int lane)
-      : m(-__builtin_inff()), l(0.f), key_frags(lane & 31, lane >> 5), value_frags(0, lane) {
+      : m(-__builtin_inff()), l(0.f), special(false), key_frags(lane & 31, lane >> 5), value_frags(0, lane) {
 #pragma unroll
     for (int d = 0; d < NV; ++d) o[d] = zero16();
   }
 
   // One tile's keys from position `key0` on, of which this lane's query sees those
-  // up to `last`.  MASKED: some query of the wave does not see all of them.
-  template <bool MASKED>
+  // up to `last`.  MASKED: some query of the wave does not see all of them; where such a
+  // tile holds a value that is not finite, `special` is set and SAFE does the block again.
+  template <bool MASKED, bool SAFE>
   __device__ __forceinline__ void step(const char* lds, int key0, int last, float c, int lane) {
     const int h = lane >> 5;
     f32x16 s[2] = {zero16(), zero16()};
-#pragma unroll
-    for (int k = 0; k < KS; ++k)
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const F key = 16 * k < DN ? key_frags.load(lds, k, 32 * t) : key_frags.load(lds + L::pe, k - DN / 16, 32 * t);
-        s[t] = mma16(key, q[k], s[t]);
-      }
+    pipelined<F, 2 * KS, 4>(
+        [&](int i) {
+          const int k = i / 2, t = i % 2;
+          return 16 * k < DN ? key_frags.load(lds, k, 32 * t) : key_frags.load(lds + L::pe, k - DN / 16, 32 * t);
+        },
+        [&](int i, F key) { s[i % 2] = mma16(key, q[i / 2], s[i % 2]); });
     if (MASKED) {
 #pragma unroll
       for (int t = 0; t < 2; ++t)
@@ -88,18 +89,17 @@ struct Prefill {
       for (int d = 0; d < NV; ++d) o[d] *= alpha;
     }
     const char* values = lds + L::v;
-    if (MASKED && __builtin_expect(special(values, lane), 0)) {
+    if (MASKED && SAFE) {
       values_special(values, p, key0, last, lane);
       return;
     }
-#pragma unroll
-    for (int d = 0; d < NV; ++d)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) o[d] = mma16(value_frags.load(values, 16 * k, d), p[k], o[d]);
+    if (MASKED) special |= not_finite(values, lane);
+    pipelined<F, 4 * NV, 2>([&](int i) { return value_frags.load(values, 16 * (i % 4), i / 4); },
+                            [&](int i, F value) { o[i / 4] = mma16(value, p[i % 4], o[i / 4]); });
   }
 
   // Whether a tile holds a value that is not finite.
-  static __device__ __forceinline__ bool special(const char* values, int lane) {
+  static __device__ __forceinline__ bool not_finite(const char* values, int lane) {
     bool any = false;
 #pragma unroll
     for (int b = 0; b < L::kv * KB * 128 / 1024; ++b) {
@@ -113,22 +113,21 @@ struct Prefill {
           any |= (w[i] & 0x7f800000u) == 0x7f800000u;
       }
     }
-    return __any(any);
+    return any;
   }
   __device__ __forceinline__ void values_special(const char* values, const F (&p)[4], int key0, int last, int lane) {
     const int h = lane >> 5;
 #pragma unroll
     for (int d = 0; d < NV; ++d) {
       f32x16 kinds = zero16();
-#pragma unroll 1
+#pragma unroll
       for (int k = 0; k < 4; ++k) {
-        F v = value_frags.load(values, 16 * k, d), kind, sees, w;
+        F v = value_frags.load(values, 16 * k, d), kind, sees;
         split_special(v, kind);
 #pragma unroll
         for (int e = 0; e < 8; ++e)
           sees[e] = from_f32<T>(key0 + 16 * k + 8 * (e >> 2) + 4 * h + (e & 3) <= last ? 1.f : 0.f);
-        w = k == 0 ? p[0] : k == 1 ? p[1] : k == 2 ? p[2] : p[3];
-        o[d] = mma16(v, w, o[d]);
+        o[d] = mma16(v, p[k], o[d]);
         kinds = mma16(kind, sees, kinds);
       }
 #pragma unroll
@@ -137,31 +136,16 @@ struct Prefill {
   }
 };
 
-template <typename T, int DN, int DR, int DV>
-__global__ __launch_bounds__(THREADS, sizeof(T) == 2 ? 2 : 1) void latent_prefill_kernel(LatentPrefillArgs a, int blocks, int classes) {
+// Queries first .. first + QB - 1 of a sequence, of one head: its queries begin at q0, its
+// keys at k0.
+template <typename T, int DN, int DR, int DV, bool SAFE>
+__device__ __forceinline__ bool prefill_block(const LatentPrefillArgs& a, char* even, char* odd, int head, int first,
+                                              int q0, int queries, int k0, int keys) {
   using P = Prefill<T, DN, DR, DV>;
   using L = Tile<T, DN, DR, DV>;
   constexpr int ES = sizeof(T);
-  __shared__ __attribute__((aligned(128))) char even[L::bytes], odd[L::bytes];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, h = lane >> 5;
-
-  // Workgroups go round the 8 XCDs; those of one XCD take the heads of one class, a
-  // head after the other, so that the workgroups that run together there read the
-  // same keys through its L2.  Late queries, which see most keys, go first.
-  const int xcd = blockIdx.x & 7, per = 8 / classes, i = blockIdx.x >> 3;
-  const int nb = (blocks + per - 1) / per;
-  const int head = xcd / per + classes * (i / nb);
-  const int back = xcd % per + per * (i % nb);
-  if (back >= blocks) return;
-  const int64_t b = blocks - 1 - back;
-  const int n = find_sequence<QB>(a.cu, a.n_seqs, a.q_total, 1, b);
-  const int q0 = a.cu ? seq_start(a.cu, n, a.q_total) : 0, q1 = a.cu ? seq_start(a.cu, n + 1, a.q_total) : a.q_total;
-  const int64_t block = b - first_block<QB>(q0, 1, n);
-  if (block < 0 || block * QB >= q1 - q0) return;
-  const int32_t* cu_k = a.cu_k ? a.cu_k : a.cu;
-  const int k0 = cu_k ? seq_start(cu_k, n, a.k_total) : 0, k1 = cu_k ? seq_start(cu_k, n + 1, a.k_total) : a.k_total;
-  const int keys = max(k1 - k0, 0), queries = q1 - q0;
-  const int first = (int)block * QB, mine = first + 32 * wave + (lane & 31);
+  const int lane = threadIdx.x & 63, wave = wave_index(), h = lane >> 5;
+    const int mine = first + 32 * wave + (lane & 31);
   const int last = mine + (keys - queries);                     // the last key this lane's query sees
   const int wave_last = first + 32 * wave + (keys - queries);   // the last one that all of the wave's see
   // keys that the workgroup's last query sees
@@ -207,9 +191,9 @@ __global__ __launch_bounds__(THREADS, sizeof(T) == 2 ? 2 : 1) void latent_prefil
   };
   auto work = [&](int t, const char* tile) {
     if (__builtin_expect(t * KB + KB - 1 <= wave_last, 1))
-      s.template step<false>(tile, t * KB, last, c, lane);
+      s.template step<false, SAFE>(tile, t * KB, last, c, lane);
     else if (t * KB <= wave_last + 31)
-      s.template step<true>(tile, t * KB, last, c, lane);
+      s.template step<true, SAFE>(tile, t * KB, last, c, lane);
   };
   const int tiles = end > 0 ? (end + KB - 1) / KB : 0;
   if (tiles > 0) fetch(0, even);
@@ -223,7 +207,17 @@ __global__ __launch_bounds__(THREADS, sizeof(T) == 2 ? 2 : 1) void latent_prefil
     work(t + 1, odd);
   }
 
-  if (mine >= queries) return;
+  if (!SAFE) {  // (the flags go where the tiles were: there is no room beside them)
+    int* flags = reinterpret_cast<int*>(even);
+    const bool special = __any(s.special);
+    __syncthreads();
+    if (lane == 0) flags[wave] = special;
+    __syncthreads();
+    const int any = flags[0] | flags[1] | flags[2] | flags[3];
+    __syncthreads();
+    if (any) return false;
+  }
+  if (mine >= queries) return true;
   const float sum = s.l + other_half(s.l);
   const float inv = last >= 0 ? 1.f / sum : 0.f;  // no key: O is 0
   T* row = static_cast<T*>(a.o) + (int64_t)(q0 + mine) * a.o_stride + (int64_t)head * DV;
@@ -236,6 +230,31 @@ __global__ __launch_bounds__(THREADS, sizeof(T) == 2 ? 2 : 1) void latent_prefil
       for (int e = 0; e < 4; ++e) y[e] = from_f32<T>(s.o[d][4 * g + e] * inv);
       *reinterpret_cast<typename Vec4<T>::type*>(row + 32 * d + 8 * g + 4 * h) = y;
     }
+  return true;
+}
+
+template <typename T, int DN, int DR, int DV>
+__global__ __launch_bounds__(THREADS, sizeof(T) == 2 ? 2 : 1) void latent_prefill_kernel(LatentPrefillArgs a, int blocks, int classes) {
+  using L = Tile<T, DN, DR, DV>;
+  __shared__ __attribute__((aligned(128))) char even[L::bytes], odd[L::bytes];
+  // Workgroups go round the 8 XCDs; those of one XCD take the heads of one class, a
+  // head after the other, so that the workgroups that run together there read the
+  // same keys through its L2.  Late queries, which see most keys, go first.
+  const int xcd = blockIdx.x & 7, per = 8 / classes, i = blockIdx.x >> 3;
+  const int nb = (blocks + per - 1) / per;
+  const int head = xcd / per + classes * (i / nb);
+  const int back = xcd % per + per * (i % nb);
+  if (back >= blocks) return;
+  const int64_t b = blocks - 1 - back;
+  const int n = find_sequence<QB>(a.cu, a.n_seqs, a.q_total, 1, b);
+  const int q0 = a.cu ? seq_start(a.cu, n, a.q_total) : 0, q1 = a.cu ? seq_start(a.cu, n + 1, a.q_total) : a.q_total;
+  const int64_t block = b - first_block<QB>(q0, 1, n);
+  if (block < 0 || block * QB >= q1 - q0) return;
+  const int32_t* cu_k = a.cu_k ? a.cu_k : a.cu;
+  const int k0 = cu_k ? seq_start(cu_k, n, a.k_total) : 0, k1 = cu_k ? seq_start(cu_k, n + 1, a.k_total) : a.k_total;
+  const int first = (int)block * QB, keys = max(k1 - k0, 0);
+  if (!prefill_block<T, DN, DR, DV, false>(a, even, odd, head, first, q0, q1 - q0, k0, keys))
+    prefill_block<T, DN, DR, DV, true>(a, even, odd, head, first, q0, q1 - q0, k0, keys);
 }
 
 template <typename T, int DN, int DR, int DV>
