@@ -21,7 +21,12 @@ using kda::row_set;
 using kda::RowSet;
 
 constexpr int64_t kMaxStride = (int64_t)1 << 28;
-constexpr int64_t kMaxKeyStride = (int64_t)1 << 22;
+// Of rows that a workgroup addresses from its first one: keeps the byte offsets of 128 of
+// them in 31 bits.
+constexpr int64_t kMaxRowStride = (int64_t)1 << 22;
+constexpr int64_t kMaxSequences = (int64_t)1 << 24;
+// A kernel counts positions some tiles past the last one.
+constexpr int64_t kMaxPositions = INT32_MAX - 256;
 constexpr int64_t kMaxTokens = INT32_MAX - 64;
 // Workgroups of a launch: threads stay below 2^32.
 constexpr int64_t kMaxBlocks = (int64_t)1 << 23;
@@ -63,8 +68,8 @@ RowSet head_rows(const void* p, int64_t rows, int64_t stride, int64_t heads, int
 int check_pages(int32_t dtype, int32_t n_seqs, int32_t dc, int32_t dr, int32_t page_size, int32_t max_pages,
                 int32_t n_pages, int64_t page_stride, int64_t row_stride, int64_t t_total, bool cu, kda::LatentPages* g) {
   if (!dtype_ok(dtype)) return KDA_ERR_DTYPE;
-  if (n_seqs < 0 || page_size < 1 || max_pages < 1 || n_pages < 0 || !tokens_ok(t_total) ||
-      (int64_t)max_pages * page_size > kMaxTokens || (!cu && t_total != n_seqs))
+  if (n_seqs < 0 || n_seqs > kMaxSequences || page_size < 1 || max_pages < 1 || n_pages < 0 || !tokens_ok(t_total) ||
+      (int64_t)max_pages * page_size > kMaxPositions || (!cu && t_total != n_seqs))
     return KDA_ERR_SHAPE;
   if ((dc != 256 && dc != 512) || (dr != 32 && dr != 64)) return KDA_ERR_UNSUPPORTED;
   const int64_t es = dtype == KDA_DTYPE_BF16 ? 2 : 4;
@@ -117,7 +122,7 @@ int check_attend(const kda_latent_attend_desc* d, kda::LatentAttendArgs* a) {
       (st = check_stride(d->o_stride, H * d->dc, es, &a->o_stride)) != KDA_OK)
     return st;
   // (token, head) rows are counted in 32 bits
-  if (d->t_total * H > kMaxTokens)
+  if (a->o_stride > kMaxRowStride || d->t_total * H > kMaxTokens)
     return KDA_ERR_SHAPE;
   a->bf16 = d->dtype == KDA_DTYPE_BF16;
   a->n_heads = d->n_heads;
@@ -158,8 +163,9 @@ int kda_latent_prefill(const kda_latent_prefill_desc* d, void* stream) {
   for (const void* p : p16)
     if (!aligned(p, 16)) return KDA_ERR_ALIGN;
   if (!aligned(d->cu_seqlens, 4) || !aligned(d->cu_seqlens_k, 4)) return KDA_ERR_ALIGN;
-  // keeps the byte offsets of a tile of 64 keys in 31 bits
-  if (a.k_stride > kMaxKeyStride || a.pe_stride > kMaxKeyStride || a.v_stride > kMaxKeyStride) return KDA_ERR_SHAPE;
+  if (a.k_stride > kMaxRowStride || a.pe_stride > kMaxRowStride || a.v_stride > kMaxRowStride ||
+      a.o_stride > kMaxRowStride)
+    return KDA_ERR_SHAPE;
   const RowSet o = row_set(d->o, T, a.o_stride, H * dv, es);
   const RowSet ins[] = {row_set(d->q, T, a.q_stride, H * (dn + dr), es),
                         head_rows(d->k, K, a.k_stride, H, a.k_head, dn, es), row_set(d->k_pe, K, a.pe_stride, dr, es),

@@ -22,7 +22,11 @@ namespace {
 
 constexpr int JOIN_THREADS = 256;
 constexpr int RUNS = 256;     // workgroups: their tiles in LDS leave room for one per CU
-constexpr int MIN_TILES = 2;  // of a run
+// What it costs to begin a unit's piece (its queries, the first rows' latency) and to end
+// it, in tiles: each unit counts as that many more, in front, so that a run that crosses
+// from one into another has fewer tiles for it.
+constexpr int SETUP = 3;
+constexpr int MIN_TILES = SETUP + 2;  // of a run (fp32, whose tiles are shorter and take longer: one less)
 
 // The workspace.  A run has at most two pieces of units that are cut: one that begins
 // inside its unit (place 2 run) and one that begins with it (place 2 run + 1).  The
@@ -41,7 +45,7 @@ struct Plan {
     rows = a.bf16 && T * H >= 64 * N ? 64 : 32;
     const int tile = a.bf16 ? 64 : 32;
     units = a.pages.cu ? T * H / rows + N : N * ((H + rows - 1) / rows);
-    const int64_t tiles = units * (((int64_t)a.pages.max_pages * a.pages.page_size + tile - 1) / tile);
+    const int64_t tiles = units * (SETUP + ((int64_t)a.pages.max_pages * a.pages.page_size + tile - 1) / tile) / MIN_TILES;
     runs = (int)(tiles < RUNS ? (tiles < 1 ? 1 : tiles) : RUNS);
     by_unit = units <= FEW_UNITS;
     heads = by_unit ? (int)units : runs;
@@ -52,7 +56,7 @@ struct Plan {
 };
 
 struct Workspace {
-  int4* heads;    // run of the unit's first piece, how many more follow (0: not cut), sequence, unit
+  int4* heads;    // run of the unit's first piece, how many more follow (0: not cut), first row, rows
   float* sums;    // [2 runs][R][dc]
   float2* stats;  // [2 runs][R]: maximum (of scores), sum of weights (-1: nothing seen)
   int by_unit;
@@ -63,7 +67,7 @@ struct Sequence {
   int start, tokens;        // first new token; new tokens
   int length, rows;         // seq_lens, and the rows of it that the table has places for
   int64_t units;            // of R queries
-  int tiles;                // of KB rows, of each unit (one at least)
+  int tiles;                // of KB rows, of each unit, and SETUP
   __device__ __forceinline__ int64_t all() const { return units * tiles; }
 };
 template <int R, int KB>
@@ -74,24 +78,55 @@ __device__ __forceinline__ Sequence sequence_of(const LatentPages& g, int n_head
   s.length = max(g.lens[n], 0);
   s.rows = min(s.length, g.max_pages * g.page_size);
   s.units = ((int64_t)s.tokens * n_heads + R - 1) / R;
-  s.tiles = max((s.rows + KB - 1) / KB, 1);
+  s.tiles = SETUP + max((s.rows + KB - 1) / KB, 1);
   return s;
 }
 
-// Inclusive sum over the workgroup's threads.
-__device__ __forceinline__ int64_t scan(int64_t x, int64_t* waves) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+// Inclusive sum over the workgroup's threads, and the sum of all.
+template <int WAVES>
+__device__ __forceinline__ int64_t scan(int64_t x, int64_t* waves, int64_t* all) {
+  const int lane = threadIdx.x & 63, wave = wave_index();
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
     const int64_t y = __shfl_up(x, d);
     if (lane >= d) x += y;
   }
-  __syncthreads();
   if (lane == 63) waves[wave] = x;
   __syncthreads();
-  for (int w = 0; w < wave; ++w) x += waves[w];
+  *all = 0;
+#pragma unroll
+  for (int w = 0; w < WAVES; ++w) {
+    if (w < wave) x += waves[w];
+    *all += waves[w];
+  }
   return x;
 }
+
+// a / b, in 32 bits where they do.
+__device__ __forceinline__ int64_t divide(int64_t a, int b) {
+  return a >> 32 == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
+// The tiles of all units (and SETUP each), total, in `runs` equal runs: the first `longer` of them have
+// one more than the others' `share`.
+struct Runs {
+  int64_t total, share;
+  int runs, longer;
+  __device__ __forceinline__ Runs(int64_t all, int most) : total(all) {
+    runs = (int)min((int64_t)most, max(all / MIN_TILES, (int64_t)1));
+    share = divide(all, runs);
+    longer = (int)(all - share * runs);
+  }
+  __device__ __forceinline__ int64_t begin(int run) const { return share * run + min(run, longer); }
+  // runs behind `run` that the next `rest` tiles reach into
+  __device__ __forceinline__ int reached(int run, int rest) const {
+    if (rest == 0) return 0;
+    if (share >= rest) return 1;
+    const int same = max(longer - (run + 1), 0), each = (int)share;
+    if (rest <= (int64_t)same * (each + 1)) return (rest + each) / (each + 1);
+    return same + (rest - same * (each + 1) + each - 1) / each;
+  }
+};
 
 // How NW waves share a tile of KB cached rows and a unit of R queries.  Scores: KG
 // groups of keys times RG groups of queries, a wave KT tiles of 16 x 16.
@@ -146,20 +181,20 @@ struct Attend {
   }
 
   // Whether every query of the unit sees all of the tile at j0.
-  static __device__ __forceinline__ bool whole(const uint64_t* have, int j0, int least) {
-    uint64_t all = ~(uint64_t)0;
-#pragma unroll
-    for (int g = 0; g < KB / 8; ++g) all &= have[g];
-    return j0 + KB <= least && all == ~(uint64_t)0;
+  static __device__ __forceinline__ bool whole(const uint64_t* have, int j0, int least, int lane) {
+    const bool all = __ballot(have[lane % (KB / 8)] == ~(uint64_t)0) == ~(uint64_t)0;
+    return j0 + KB <= least && all;
   }
 
   // One tile: positions j0 .. j0 + KB - 1, its rows in `tile`.  Where not all of it is seen
   // each (key, query) is looked at, and false is returned if a key that is not seen holds
   // a value that is not finite (its score is not): SAFE then does the whole unit again.
-  template <bool SAFE>
+  // fetch(b) fetches column block b of the next tile, between the score's steps (all at once
+  // they would hold the waves up).
+  template <bool SAFE, typename Fetch>
   __device__ __forceinline__ bool step(const char* tile, const uint64_t* have, char* weights, Exchange& x, int j0,
-                                       int least, float c, int lane, int wave) {
-    const bool not_whole = !whole(have, j0, least);
+                                       int least, float c, int lane, int wave, Fetch fetch) {
+    const bool not_whole = !whole(have, j0, least, lane);
     const int h = lane >> 5, col = lane & 15, grp = lane >> 4;
     const int kg = wave % S::KG, rg = wave / S::KG;
     const int key0 = kg * S::KT * 16, row = rg * 16 + col;
@@ -170,6 +205,11 @@ struct Attend {
                                    [&](int i, F key) {
                                      f32x4& acc = i / S::KT % 2 ? sd[i % S::KT] : sc[i % S::KT];
                                      acc = mma32(key, q[i / S::KT], acc);
+                                   },
+                                   [&](int g) {
+                                     constexpr int groups = (S::KS * S::KT + 3) / 4, each = (S::blocks + groups - 1) / groups;
+#pragma unroll
+                                     for (int b = g * each; b < (g + 1) * each && b < S::blocks; ++b) fetch(b);
                                    });
 #pragma unroll
     for (int k = 0; k < S::KT; ++k) sc[k] += sd[k];
@@ -199,8 +239,8 @@ struct Attend {
       for (int i = 0; i < 4; ++i) mx = fmaxf(mx, sc[k][i]);
     mx = fmaxf(mx, __shfl_xor(mx, 16));
     mx = fmaxf(mx, __shfl_xor(mx, 32));
-    if (grp == 0) x.tops[kg][row] = mx;
-    if (!SAFE && lane == 0) x.odd[wave] = odd;
+    x.tops[kg][row] = mx;  // (four lanes the same)
+    if (!SAFE) x.odd[wave] = odd;
     exchanged();
     const auto tops_of = [&](int r, float m) {
 #pragma unroll
@@ -236,9 +276,7 @@ struct Attend {
       }
     }
     if (!SAFE && __builtin_expect(not_whole, 0)) {
-#pragma unroll
-      for (int w = 0; w < S::NW; ++w) odd |= x.odd[w] != 0;
-      if (odd) return false;
+      if (__any(x.odd[lane % S::NW])) return false;
     }
     exchanged();
 
@@ -298,9 +336,7 @@ struct Attend {
 // What a workgroup does of a unit: tiles tile0 .. tile1 - 1 of it.
 struct Piece {
   int n, unit, tile0, tile1;
-  int64_t unit_at;  // where the unit's tiles begin, of all tiles of the call
-  int run, runs;
-  int64_t total;
+  int run, more;  // the run this is of, and how many behind it have the unit's rest
 };
 
 template <typename T, int DC, int DR, int R, bool SAFE>
@@ -329,35 +365,35 @@ __device__ __forceinline__ bool attend_piece(const LatentAttendArgs& a, const Wo
   // that looked up.  A wave fetches eight rows, eight lanes to 128 bytes of a row, the
   // chunks exchanged as tile_at has them; a position without a row is 0 and not seen.
   static_assert(KB == 8 * S::NW, "a wave fetches eight rows of a tile");
-  const int fetch_row = 8 * wave + (lane >> 3), chunk = ((lane & 7) ^ (lane >> 3)) * 16;
+  const int fetch_row = 8 * wave + (lane >> 3), chunk = ((lane & 7) ^ row_swap(lane >> 3)) * 16;
   int page = -1;
+  const char* from;
+  const int32_t* const pages = g.table + (int64_t)n_now * g.max_pages;
   const auto look_up = [&](int tile) {
     const int j = tile * KB + fetch_row;
-    page = -1;
-    if (tile < tiles_end && j < s.rows) page = g.table[(int64_t)n_now * g.max_pages + page_of(g, j)];
+    const int p = pages[min(page_of(g, j), g.max_pages - 1)];
+    page = tile < tiles_end && j < s.rows ? p : -1;
   };
-  const auto fetch = [&](int tile, char* to, uint64_t* have) {
+  // the rows of `tile`, whose pages have been looked up; those of the tile behind it
+  const auto aim = [&](int tile, uint64_t* have) {
     const int j = tile * KB + fetch_row;
     const bool in = page >= 0 && page < g.n_pages;
-    const uint64_t there = __ballot(in);
-    if (lane == 0) have[wave] = there;
-    const char* from = reinterpret_cast<const char*>(kNoRow) + chunk;
-    if (in)
-      from = static_cast<const char*>(a.cache) +
-             ((int64_t)page * g.page_stride + row_in_page(g, j, page_of(g, j)) * g.row_stride) * ES + chunk;
-#pragma unroll
-    for (int b = 0; b < S::blocks; ++b) {
-      const char* p = from + 128 * b;
-      if (128 * (b + 1) > W * ES && 128 * b + chunk >= W * ES) p = reinterpret_cast<const char*>(kNoRow);
-      fetch16(p, to + (b * KB + 8 * wave) * 128);
-    }
+    have[wave] = __ballot(in);
+    const int64_t at = (int64_t)page * g.page_stride + row_in_page(g, j, page_of(g, j)) * g.row_stride;
+    const char* const row = static_cast<const char*>(a.cache) + at * ES;
+    from = (in ? row : reinterpret_cast<const char*>(kNoRow)) + chunk;
     look_up(tile + 1);
+  };
+  // column block b of them, one after the other
+  const auto fetch = [&](int b, char* to) {
+    const char* p = from;
+    if (128 * (b + 1) > W * ES && 128 * b + chunk >= W * ES) p = reinterpret_cast<const char*>(kNoRow);
+    fetch16(p, to + (b * KB + 8 * wave) * 128);
+    if (b + 1 < S::blocks) from = next_line(from);
   };
 
   A s_(lane, wave);
   look_up(tile0);
-  __syncthreads();  // LDS of the piece before is done with
-  if (tile0 < tiles_end) fetch(tile0, even, x.have[0]);
   const int kg = wave % S::KG, rg = wave / S::KG;
   {
     const int r = min(row0 + rg * 16 + col, n_rows - 1), tok = r / a.n_heads;
@@ -366,20 +402,29 @@ __device__ __forceinline__ bool attend_piece(const LatentAttendArgs& a, const Wo
 #pragma unroll
     for (int k = 0; k < S::KS; ++k) s_.q[k] = load_frag8<T>(qr + 32 * k + 8 * grp);
   }
+  fetched();  // LDS of the piece before is done with
+  aim(tile0, x.have[0]);
+#pragma unroll
+  for (int b = 0; b < S::blocks; ++b) fetch(b, even);
 #pragma unroll
   for (int v = 0; v < S::RV; ++v) s_.my_limit[v] = limit_of(32 * v + (lane & 31));
+  // (behind the last tile rows that do not exist are fetched)
   for (int tile = tile0; tile < tiles_end; tile += 2) {
     fetched();
-    if (tile + 1 < tiles_end) fetch(tile + 1, odd, x.have[1]);
-    if (!s_.template step<SAFE>(even, x.have[0], weights, x, tile * KB, least, c, lane, wave)) return false;
+    aim(tile + 1, x.have[1]);
+    if (!s_.template step<SAFE>(even, x.have[0], weights, x, tile * KB, least, c, lane, wave,
+                                [&](int b) { fetch(b, odd); }))
+      return false;
     if (tile + 1 == tiles_end) break;
     fetched();
-    if (tile + 2 < tiles_end) fetch(tile + 2, even, x.have[0]);
-    if (!s_.template step<SAFE>(odd, x.have[1], weights, x, (tile + 1) * KB, least, c, lane, wave)) return false;
+    aim(tile + 2, x.have[0]);
+    if (!s_.template step<SAFE>(odd, x.have[1], weights, x, (tile + 1) * KB, least, c, lane, wave,
+                                [&](int b) { fetch(b, even); }))
+      return false;
   }
+  fetched();
 
   // the sum of weights of each row, over lanes and waves
-  __syncthreads();
   {
     float y = s_.sum;
     y += __shfl_xor(y, 16);
@@ -387,15 +432,17 @@ __device__ __forceinline__ bool attend_piece(const LatentAttendArgs& a, const Wo
     int any = s_.seen;
     any |= __shfl_xor(any, 16);
     any |= __shfl_xor(any, 32);
-    if (grp == 0) x.sums[kg][rg * 16 + col] = y, x.seen[kg][rg * 16 + col] = any;
+    x.sums[kg][rg * 16 + col] = y;
+    x.seen[kg][rg * 16 + col] = any;
   }
   __syncthreads();
-  if (tile0 == 0 && threadIdx.x == 0) {
-    // the unit's last piece is in the last run that begins before the unit ends
-    const int more = (int)(((pc.unit_at + s.tiles) * pc.runs + pc.total - 1) / pc.total) - 1 - run;
+  if (tile0 == 0 && wave == 0) {
     const int64_t id = g.cu ? first_block<R>(s.start, a.n_heads, n_now) : (int64_t)n_now * s.units;
-    if (ws.by_unit || more > 0) ws.heads[ws.by_unit ? id + unit : run] = int4{run, more, n_now, unit};
+    if (ws.by_unit || pc.more > 0)
+      ws.heads[ws.by_unit ? id + unit : run] = int4{run, pc.more, s.start * a.n_heads + row0, min(n_rows - row0, R)};
   }
+  const int tok0 = row0 / a.n_heads;
+  const auto out = make_rsrc(static_cast<char*>(a.o) + (s.start + tok0) * a.o_stride * ES, INT32_MAX);
 #pragma unroll
   for (int v = 0; v < S::RV; ++v) {
     const int r = 32 * v + (lane & 31);
@@ -403,12 +450,10 @@ __device__ __forceinline__ bool attend_piece(const LatentAttendArgs& a, const Wo
     int some = 0;
 #pragma unroll
     for (int k = 0; k < S::KG; ++k) all += x.sums[k][r], some |= x.seen[k][r];
-    if (tile0 == 0 && tile1 == s.tiles) {
-      if (row0 + r >= n_rows) continue;
+    if (tile0 == 0 && tile1 == s.tiles - SETUP) {
       const int tok = (row0 + r) / a.n_heads;
-      const float inv = some ? 1.f / all : 0.f;  // no key: O is 0
-      T* out = static_cast<T*>(a.o) + (s.start + tok) * a.o_stride + (int64_t)(row0 + r - tok * a.n_heads) * DC +
-               S::COLS * wave;
+      const int at = (int)((tok - tok0) * a.o_stride + (row0 + r - tok * a.n_heads) * DC + S::COLS * wave + 4 * h) * ES;
+      const float inv = some ? __builtin_amdgcn_rcpf(all) : 0.f;  // no key: O is 0
 #pragma unroll
       for (int d = 0; d < S::NV; ++d)
 #pragma unroll
@@ -416,20 +461,21 @@ __device__ __forceinline__ bool attend_piece(const LatentAttendArgs& a, const Wo
           typename Vec4<T>::type y;
 #pragma unroll
           for (int e = 0; e < 4; ++e) y[e] = from_f32<T>(s_.o[d][v][4 * b + e] * inv);
-          *reinterpret_cast<typename Vec4<T>::type*>(out + 32 * d + 8 * b + 4 * h) = y;
+          store4(y, out, row0 + r < n_rows ? at + (32 * d + 8 * b) * ES : kBufferOff);
         }
     } else {
       const int64_t place = 2 * (int64_t)run + (tile0 == 0 ? 1 : 0);
-      float* out = ws.sums + (place * R + r) * DC + S::COLS * wave;
+      float* sums = ws.sums + (place * R + r) * DC + S::COLS * wave;
 #pragma unroll
       for (int d = 0; d < S::NV; ++d)
 #pragma unroll
         for (int b = 0; b < 4; ++b)
-          *reinterpret_cast<f32x4*>(out + 32 * d + 8 * b + 4 * h) =
+          *reinterpret_cast<f32x4*>(sums + 32 * d + 8 * b + 4 * h) =
               f32x4{s_.o[d][v][4 * b], s_.o[d][v][4 * b + 1], s_.o[d][v][4 * b + 2], s_.o[d][v][4 * b + 3]};
-      if (wave == 0 && lane < 32) ws.stats[place * R + r] = float2{s_.top_o[v], some ? all : -1.f};
+      if (wave == 0) ws.stats[place * R + r] = float2{s_.top_o[v], some ? all : -1.f};
     }
   }
+  end_of_variant<SAFE>();
   return true;
 }
 
@@ -448,68 +494,56 @@ __global__ __launch_bounds__((Shape<T, DC, DR, R>::THREADS), 1) void latent_atte
   // this workgroup's run of tiles, and the sequence it begins in
   const int run = blockIdx.x;
   if (!ws.by_unit && threadIdx.x == 0) ws.heads[run].y = 0;
-  int64_t total = 0;
-  for (int base = 0; base < g.n_seqs; base += THREADS) {
-    const int n = base + threadIdx.x;
-    int64_t y = 0;
-    if (n < g.n_seqs) y = sequence_of<R, KB>(g, a.n_heads, n).all();
-    y = scan(y, waves);
-    __syncthreads();
-    if (threadIdx.x == THREADS - 1) found[0] = y;
-    __syncthreads();
-    total += found[0];
-  }
-  const int runs = (int)min((int64_t)gridDim.x, max(total / MIN_TILES, (int64_t)1));
-  const auto bound = [&](int64_t r) { return total * r / runs; };
-  if (run >= runs) return;
-  const int64_t lo = bound(run), hi = bound(run + 1);
+  // (a thread sums up the tiles of some neighbouring sequences, and the one that has the
+  // run's first tile among its own looks for it there)
+  const int each = (g.n_seqs - 1) / THREADS + 1, first = min((int)threadIdx.x * each, g.n_seqs);
+  int64_t mine = 0, total;
+  for (int i = first; i < min(first + each, g.n_seqs); ++i) mine += sequence_of<R, KB>(g, a.n_heads, i).all();
+  const int64_t upto = scan<S::NW>(mine, waves, &total);
+  const Runs runs(uniform(total), gridDim.x);
+  if (run >= runs.runs) return;
+  const int64_t lo = runs.begin(run), hi = runs.begin(run + 1);
   if (lo >= hi) return;
-  int64_t before = 0;
-  for (int base = 0;; base += THREADS) {
-    const int n = base + threadIdx.x;
-    int64_t y = 0;
-    if (n < g.n_seqs) y = sequence_of<R, KB>(g, a.n_heads, n).all();
-    const int64_t upto = before + scan(y, waves);
-    if (y > 0 && upto - y <= lo && lo < upto) {
-      found[0] = n;
-      found[1] = upto - y;
+  if (mine > 0 && upto - mine <= lo && lo < upto) {
+    int64_t at = upto - mine;
+    int i = first;
+    for (; i < first + each - 1 && i < g.n_seqs - 1; ++i) {
+      const int64_t y = sequence_of<R, KB>(g, a.n_heads, i).all();
+      if (lo < at + y) break;
+      at += y;
     }
-    __syncthreads();
-    if (threadIdx.x == THREADS - 1) waves[0] = upto;
-    __syncthreads();
-    before = waves[0];
-    if (lo < before) break;
+    found[0] = i;
+    found[1] = at;
   }
-  int n = (int)found[0];
-  int64_t seq_at = found[1];  // the tile that the sequence's first unit begins with
+  __syncthreads();
+  int n = uniform((int)found[0]);
+  int64_t seq_at = uniform(found[1]);  // the tile that the sequence's first unit begins with
 
   for (int64_t pos = lo; pos < hi;) {
     const Sequence s = sequence_of<R, KB>(g, a.n_heads, n);
     const int64_t in_seq = pos - seq_at;
-    const int unit = (int)(in_seq / s.tiles), tile0 = (int)(in_seq - (int64_t)unit * s.tiles);
-    const int tile1 = (int)min((int64_t)s.tiles, tile0 + (hi - pos));
-    const int64_t unit_at = pos - tile0;
-    pos += tile1 - tile0;
-    const int n_now = n;
-    if (pos - seq_at == s.all()) {
+    const int unit = (int)divide(in_seq, s.tiles), from = (int)(in_seq - (int64_t)unit * s.tiles);
+    const int to = (int)min((int64_t)s.tiles, from + (hi - pos));
+    pos += to - from;
+    const Piece pc = {n, unit, max(from - SETUP, 0), max(to - SETUP, 0), run, runs.reached(run, s.tiles - to)};
+    if (pos - seq_at >= s.all()) {
       seq_at = pos;
       ++n;
-      while (pos < hi && n + 1 < g.n_seqs && sequence_of<R, KB>(g, a.n_heads, n).units == 0) ++n;
+      while (n < g.n_seqs && sequence_of<R, KB>(g, a.n_heads, n).units == 0) ++n;
     }
-
-    const Piece pc = {n_now, unit, tile0, tile1, unit_at, run, runs, total};
-    if (!attend_piece<T, DC, DR, R, false>(a, ws, s, pc, even, odd, weights, x))
+    if (pc.tile1 > 0 && !attend_piece<T, DC, DR, R, false>(a, ws, s, pc, even, odd, weights, x))
       attend_piece<T, DC, DR, R, true>(a, ws, s, pc, even, odd, weights, x);
+    if (n >= g.n_seqs) break;
   }
 }
 
 // The rows of units that were cut: the pieces' sums, each at its own maximum, brought
-// to the largest.  A workgroup takes 128 columns of a row at a time, eight groups of 32
-// threads every eighth piece each; `shares` workgroups share a unit.
-template <typename T, int DC, int R, int KB>
+// to the largest.  A workgroup takes COLS columns of a row at a time, its threads in
+// groups of COLS / 4 with every so many-th piece each; `shares` workgroups share a unit.
+template <typename T, int DC, int R, int KB, int COLS>
 __global__ __launch_bounds__(JOIN_THREADS) void latent_join_kernel(LatentAttendArgs a, Workspace ws, int shares) {
-  constexpr int PARTS = DC / 128, GROUPS = 8;
-  __shared__ float factors[RUNS], wide[GROUPS][128];
+  constexpr int PARTS = DC / COLS, WIDTH = COLS / 4, GROUPS = JOIN_THREADS / WIDTH;
+  __shared__ float factors[RUNS], wide[GROUPS][COLS];
   __shared__ float tops[4], sums[4];
   __shared__ int some_by[4];
   const LatentPages& g = a.pages;
@@ -523,14 +557,12 @@ __global__ __launch_bounds__(JOIN_THREADS) void latent_join_kernel(LatentAttendA
   const int4 head = ws.heads[id];
   const int more = head.y;
   if (more == 0) return;
-  const Sequence s = sequence_of<R, KB>(g, a.n_heads, head.z);
-  const int row0 = head.w * R, n_rows = s.tokens * a.n_heads;
   const float c = a.scale * kLog2e;
   const int i = threadIdx.x, lane = i & 63, wave = i >> 6;
-  const int group = i / 32, at = 4 * (i & 31);
+  const int group = i / WIDTH, at = 4 * (i % WIDTH);
   for (int item = blockIdx.x % shares; item < R * PARTS; item += shares) {
     const int part = item % PARTS, r = item / PARTS;
-    if (row0 + r >= n_rows) return;
+    if (r >= head.w) return;
     const auto place = [&](int k) { return ((int64_t)(k == 0 ? 2 * head.x + 1 : 2 * (head.x + k)) * R + r); };
     // a piece each thread: at most RUNS of them
     const float2 st = i <= more ? ws.stats[place(i)] : float2{0.f, -1.f};
@@ -554,18 +586,18 @@ __global__ __launch_bounds__(JOIN_THREADS) void latent_join_kernel(LatentAttendA
     f32x4 o = zero4();
 #pragma unroll 4
     for (int k = group; k <= more; k += GROUPS)
-      o += factors[k] * *reinterpret_cast<const f32x4*>(ws.sums + place(k) * DC + 128 * part + at);
+      o += factors[k] * *reinterpret_cast<const f32x4*>(ws.sums + place(k) * DC + COLS * part + at);
     *reinterpret_cast<f32x4*>(&wide[group][at]) = o;
     __syncthreads();
-    if (i < 128) {
+    sum = (sums[0] + sums[1]) + (sums[2] + sums[3]);
+    const float inv = some_by[0] | some_by[1] | some_by[2] | some_by[3] ? 1.f / sum : 0.f;
+    const int row = head.z + r, tok = row / a.n_heads;
+    T* out = static_cast<T*>(a.o) + (int64_t)tok * a.o_stride + (int64_t)(row - tok * a.n_heads) * DC + COLS * part;
+    for (int col = i; col < COLS; col += JOIN_THREADS) {
       float y = 0.f;
 #pragma unroll
-      for (int k = 0; k < GROUPS; ++k) y += wide[k][i];
-      sum = (sums[0] + sums[1]) + (sums[2] + sums[3]);
-      const float inv = some_by[0] | some_by[1] | some_by[2] | some_by[3] ? 1.f / sum : 0.f;
-      const int tok = (row0 + r) / a.n_heads;
-      static_cast<T*>(a.o)[(s.start + tok) * a.o_stride + (int64_t)(row0 + r - tok * a.n_heads) * DC + 128 * part + i] =
-          from_f32<T>(y * inv);
+      for (int k = 0; k < GROUPS; ++k) y += wide[k][col];
+      out[col] = from_f32<T>(y * inv);
     }
   }
 }
@@ -574,9 +606,12 @@ template <typename T, int DC, int DR, int R>
 hipError_t run(const LatentAttendArgs& a, const Plan& plan, const Workspace& ws, hipStream_t stream) {
   hipError_t e = enqueue(latent_attend_kernel<T, DC, DR, R>, (unsigned)plan.runs, Shape<T, DC, DR, R>::THREADS, stream, a, ws);
   if (e != hipSuccess) return e;
-  const int shares = plan.by_unit ? R * (DC / 128) : 16;
-  return enqueue(latent_join_kernel<T, DC, R, Shape<T, DC, DR, R>::KB>, (unsigned)(plan.heads * shares), JOIN_THREADS, stream,
-                 a, ws, shares);
+  constexpr int KB = Shape<T, DC, DR, R>::KB;
+  if (plan.units <= FEW_UNITS / 8)  // their rows alone would not fill the GPU
+    return enqueue(latent_join_kernel<T, DC, R, KB, 128>, (unsigned)(plan.heads * R * (DC / 128)), JOIN_THREADS, stream, a,
+                   ws, R * (DC / 128));
+  const int shares = plan.by_unit ? R : 16;
+  return enqueue(latent_join_kernel<T, DC, R, KB, DC>, (unsigned)(plan.heads * shares), JOIN_THREADS, stream, a, ws, shares);
 }
 
 template <typename T, int R>

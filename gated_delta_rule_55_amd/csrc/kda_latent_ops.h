@@ -43,12 +43,14 @@ __device__ __forceinline__ f32x16 zero16() {
 __device__ __forceinline__ int row_of(int h, int i) { return 8 * (i >> 2) + 4 * h + (i & 3); }
 
 // A tile of ROWS rows in LDS.  Rows are cut into column blocks of 128 bytes, each
-// block a [ROWS][128 bytes] array whose 16-byte chunks are exchanged by the row's
-// low three bits: eight rows' chunks of one column lie in different banks, and
-// eight lanes that fetch a 128-byte line fill 128 consecutive bytes.
+// block a [ROWS][128 bytes] array whose 16-byte chunks are exchanged by a number of the
+// row: eight rows' chunks of one column lie in different banks, and so do 64 bytes of
+// rows r and r + 2 (banks repeat after 256 bytes, two rows), which a transposing read
+// fetches together.
+__device__ __forceinline__ int row_swap(int row) { return (row & 1) | (row & 2) << 1 | (row & 4) >> 1; }
 template <int ROWS>
 __device__ __forceinline__ int tile_at(int row, int byte) {
-  return (byte >> 7) * (ROWS * 128) + row * 128 + ((((byte >> 4) & 7) ^ (row & 7)) << 4) + (byte & 15);
+  return (byte >> 7) * (ROWS * 128) + row * 128 + ((((byte >> 4) & 7) ^ row_swap(row)) << 4) + (byte & 15);
 }
 
 // A value that the compiler keeps in a register as it is: an address that constants
@@ -127,10 +129,10 @@ struct ColFrags {
 
 // N matrix steps whose operands come from LDS, in groups of G: a group's operands are
 // read while the group before runs.  (Left to itself the compiler reads each operand
-// right before its step, where registers are short.)  load(i) answers step i's operand
-// and step(i, operand) runs it.
-template <typename F, int N, int G, typename Load, typename Step>
-__device__ __forceinline__ void pipelined(Load load, Step step) {
+// right before its step, where registers are short.)  load(i) answers step i's operand,
+// step(i, operand) runs it, and between(g) is other work for behind group g's steps.
+template <typename F, int N, int G, typename Load, typename Step, typename Between>
+__device__ __forceinline__ void pipelined(Load load, Step step, Between between) {
   F now[G], next[G];
 #pragma unroll
   for (int i = 0; i < G; ++i) now[i] = load(i);
@@ -143,10 +145,15 @@ __device__ __forceinline__ void pipelined(Load load, Step step) {
 #pragma unroll
     for (int i = 0; i < G; ++i)
       if (g + i < N) step(g + i, now[i]);
+    between(g / G);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int i = 0; i < G; ++i) now[i] = next[i];
   }
+}
+template <typename F, int N, int G, typename Load, typename Step>
+__device__ __forceinline__ void pipelined(Load load, Step step) {
+  pipelined<F, N, G>(load, step, [](int) {});
 }
 
 // Values that are not finite, in rows that some of a tile's queries see and
@@ -191,6 +198,13 @@ __device__ __forceinline__ void fetch16(const char* from, char* at) {
   typedef const __attribute__((address_space(1))) void* global;
   __builtin_amdgcn_global_load_lds((global)from, (lds)at, 16, 0, 0);
 }
+// p + 128.  (Written out: the compiler adds to 64-bit addresses from scalar registers, a
+// pair for each multiple of 128, and runs out of them.)
+__device__ __forceinline__ const char* next_line(const char* p) {
+  uint32_t lo = (uint32_t)(uintptr_t)p, hi = (uint32_t)((uintptr_t)p >> 32);
+  asm("v_add_co_u32 %0, vcc, 0x80, %0\n\tv_addc_co_u32 %1, vcc, 0, %1, vcc" : "+v"(lo), "+v"(hi) : : "vcc");
+  return reinterpret_cast<const char*>((uintptr_t)hi << 32 | lo);
+}
 // Waits for this wave's LDS accesses, then for the workgroup's other waves.  (Fetches
 // stay under way, which __syncthreads would wait for.)
 __device__ __forceinline__ void exchanged() {
@@ -212,6 +226,30 @@ __device__ __forceinline__ float other_half(float x) { return __shfl_xor(x, 32);
 
 // The wave of this thread in its workgroup, as a scalar.
 __device__ __forceinline__ int wave_index() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
+
+// A value that all lanes have, as a scalar.  What is read from LDS counts as different
+// in each lane otherwise, and a branch on it as one that lanes take by themselves: the
+// kernels here have none of those where registers are full, since copies that the
+// compiler makes behind such a branch, to free registers, have missed lanes.
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ __forceinline__ int64_t uniform(int64_t x) {
+  return (int64_t)((uint64_t)(uint32_t)uniform((int)(x >> 32)) << 32 | (uint32_t)uniform((int)x));
+}
+
+// Ends a variant's code in a way of its own: the compiler would share the ends of two
+// variants of a function, and move all their registers to where both have them.
+template <bool VARIANT>
+__device__ __forceinline__ void end_of_variant() {
+  asm volatile("; variant %0" : : "n"(VARIANT));
+}
+
+// Four neighbouring values of an output row; none where `off` is kBufferOff.
+__device__ __forceinline__ void store4(bf16x4 v, __amdgpu_buffer_rsrc_t r, int off) {
+  __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, v), r, off, 0, 0);
+}
+__device__ __forceinline__ void store4(f32x4 v, __amdgpu_buffer_rsrc_t r, int off) {
+  __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), r, off, 0, 0);
+}
 
 // The page of position j of a sequence (0 <= j < 2^31), and j's row there.
 __device__ __forceinline__ int page_of(const LatentPages& g, int j) {

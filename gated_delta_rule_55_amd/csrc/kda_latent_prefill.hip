@@ -162,7 +162,7 @@ __device__ __forceinline__ bool prefill_block(const LatentPrefillArgs& a, char* 
   // The next tile is fetched while one is worked on.  A wave fetches 16 rows of it,
   // eight lanes to 128 bytes of a row, the chunks exchanged as tile_at has them.
   const float c = a.scale * kLog2e;
-  const int r0 = 16 * wave + (lane >> 3), chunk = ((lane & 7) ^ (lane >> 3)) * 16;
+  const int r0 = 16 * wave + (lane >> 3), chunk = ((lane & 7) ^ row_swap(lane >> 3)) * 16;
   const int k_row = (int)a.k_stride * ES, p_row = (int)a.pe_stride * ES, v_row = (int)a.v_stride * ES;
   const char* kt = static_cast<const char*>(a.k) + (k0 * a.k_stride + head * a.k_head) * ES;
   const char* pt = static_cast<const char*>(a.pe) + k0 * a.pe_stride * ES;
@@ -211,16 +211,16 @@ __device__ __forceinline__ bool prefill_block(const LatentPrefillArgs& a, char* 
     int* flags = reinterpret_cast<int*>(even);
     const bool special = __any(s.special);
     __syncthreads();
-    if (lane == 0) flags[wave] = special;
+    flags[wave] = special;
     __syncthreads();
-    const int any = flags[0] | flags[1] | flags[2] | flags[3];
+    const bool any = __any(flags[lane & 3]);
     __syncthreads();
     if (any) return false;
   }
-  if (mine >= queries) return true;
   const float sum = s.l + other_half(s.l);
-  const float inv = last >= 0 ? 1.f / sum : 0.f;  // no key: O is 0
-  T* row = static_cast<T*>(a.o) + (int64_t)(q0 + mine) * a.o_stride + (int64_t)head * DV;
+  const float inv = last >= 0 ? __builtin_amdgcn_rcpf(sum) : 0.f;  // no key: O is 0
+  const auto out = make_rsrc(static_cast<char*>(a.o) + ((int64_t)(q0 + first) * a.o_stride + head * DV) * ES, INT32_MAX);
+  const int at = (int)((mine - first) * a.o_stride + 4 * h) * ES;
 #pragma unroll
   for (int d = 0; d < P::NV; ++d)
 #pragma unroll
@@ -228,8 +228,9 @@ __device__ __forceinline__ bool prefill_block(const LatentPrefillArgs& a, char* 
       typename Vec4<T>::type y;
 #pragma unroll
       for (int e = 0; e < 4; ++e) y[e] = from_f32<T>(s.o[d][4 * g + e] * inv);
-      *reinterpret_cast<typename Vec4<T>::type*>(row + 32 * d + 8 * g + 4 * h) = y;
+      store4(y, out, mine < queries ? at + (32 * d + 8 * g) * ES : kBufferOff);
     }
+  end_of_variant<SAFE>();
   return true;
 }
 

@@ -56,7 +56,7 @@ extern "C" {
  * Layouts: q [q_total, H, dn + dr]; k [k_total, H, dn]; k_pe [k_total, dr];
  * v [k_total, H, dv]; o [q_total, H, dv].  k and v may be slices of one buffer
  * [k_total, H, dn + dv]: besides the token stride they have a head stride.
- * The token strides of k, k_pe and v are at most 2^22, dense or not.
+ * The token strides of k, k_pe, v and o are at most 2^22, dense or not.
  * cu_seqlens [N + 1] gives the sequences' queries, cu_seqlens_k [N + 1] their
  * keys; NULL: the same as the queries' (k_total == q_total then).  Both are read
  * on the device, clamped to [0, q_total] and [0, k_total]: contents that break
@@ -89,7 +89,8 @@ int kda_latent_prefill(const kda_latent_prefill_desc* d, void* stream);
  * Layouts: q [t_total, H, dc + dr]; o [t_total, H, dc]; cache [n_pages,
  * page_size, dc + dr]; block_table [N, max_pages]; seq_lens [N].  cu_seqlens
  * [N + 1] gives the sequences' new tokens (clamped as above); NULL: one token
- * for each (t_total == N).  Rows of o outside every sequence are not written.
+ * for each (t_total == N).  Rows of o outside every sequence are not written.  The
+ * token stride of o is at most 2^22, dense or not.
  *
  * A query's result depends, bit for bit, on the whole call: the rows are shared
  * out evenly over the GPU, and where a sequence's rows are cut depends on the
@@ -97,10 +98,10 @@ int kda_latent_prefill(const kda_latent_prefill_desc* d, void* stream);
 typedef struct {
   uint32_t struct_size;        /* sizeof(kda_latent_attend_desc)                */
   int32_t dtype;               /* kda_dtype of q, cache, o                      */
-  int32_t n_seqs;              /* N >= 0 (0 = nothing to do)                    */
+  int32_t n_seqs;              /* N, 0 (nothing to do) .. 2^24                  */
   int32_t n_heads;             /* H, 1 .. 65535                                 */
   int32_t dc, dr;              /* dc 256 or 512, dr 32 or 64                    */
-  int32_t page_size;           /* >= 1; max_pages * page_size <= 2^31 - 65      */
+  int32_t page_size;           /* >= 1; max_pages * page_size <= 2^31 - 257     */
   int32_t max_pages;           /* >= 1: columns of block_table                  */
   int32_t n_pages;             /* >= 0                                          */
   float scale;                 /* > 0                                           */
