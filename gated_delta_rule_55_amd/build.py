@@ -1,7 +1,7 @@
 """Build libkda.so (HIP kernels + C ABI) for gfx950 with hipcc, and the Python
-module _fast.so on top of it, in-tree.  The library takes hipcc alone; where the
-module's tools are missing (g++, the headers of Python and torch) it is left out
-and layer.py makes every call itself.
+modules _fast.so and _fast_latent.so on top of it, in-tree.  The library takes hipcc
+alone; where the modules' tools are missing (g++, the headers of Python and torch) they
+are left out, and layer.py and latent.py make every call themselves.
 
 Usage: python -m gated_delta_rule_55_amd.build [-v]
 """
@@ -45,6 +45,7 @@ SOURCE_FLAGS = {
 # The Python module that marshals the layer calls (csrc/kda_torch.cpp): host code
 # against torch's headers, on top of libkda.so.
 FAST_OUT = os.path.join(PKG, "_fast.so")
+FAST_LATENT_OUT = os.path.join(PKG, "_fast_latent.so")  # the same for latent.py (csrc/kda_latent_torch.cpp)
 
 
 def _torch_root():
@@ -68,7 +69,7 @@ def _fast_missing():
     return ""
 
 
-def _fast_command():
+def _fast_command(source="kda_torch.cpp", out=None):
     import torch
 
     troot = _torch_root()
@@ -78,7 +79,7 @@ def _fast_command():
         os.path.join(rocm, "include"), sysconfig.get_paths()["include"])]
     return (["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-Werror", "-D__HIP_PLATFORM_AMD__",
              "-DUSE_ROCM", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"] + include +
-            [os.path.join(CSRC, "kda_torch.cpp"), "-o", FAST_OUT + ".tmp",
+            [os.path.join(CSRC, source), "-o", (out or FAST_OUT) + ".tmp",
              f"-L{os.path.join(troot, 'lib')}", "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_python",
              f"-L{PKG}", "-l:libkda.so", "-Wl,-rpath,$ORIGIN"])
 
@@ -103,6 +104,20 @@ def build_fast(verbose: bool = False):
     subprocess.run(cmd, check=True)
     os.replace(FAST_OUT + ".tmp", FAST_OUT)
     return FAST_OUT
+
+
+def build_fast_latent(verbose: bool = False):
+    """build_fast for the module behind latent.py."""
+    if _fast_missing():
+        if os.path.exists(FAST_LATENT_OUT):
+            os.remove(FAST_LATENT_OUT)
+        return None
+    cmd = _fast_command("kda_latent_torch.cpp", FAST_LATENT_OUT)
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True)
+    os.replace(FAST_LATENT_OUT + ".tmp", FAST_LATENT_OUT)
+    return FAST_LATENT_OUT
 
 
 def build(verbose: bool = False, jobs: int = 4) -> str:
@@ -139,6 +154,7 @@ def build(verbose: bool = False, jobs: int = 4) -> str:
     subprocess.run(cmd, check=True)
     os.replace(OUT + ".tmp", OUT)
     build_fast(verbose)
+    build_fast_latent(verbose)
     if verbose:
         print(f"built {OUT} in {time.time() - t0:.1f}s", flush=True)
     return OUT

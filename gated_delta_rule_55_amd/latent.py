@@ -19,7 +19,11 @@ page of the cache (past the table, or a page number outside it) is neither
 written nor seen.
 
 Calls run on the device of their tensors, on `stream` or that device's current
-stream; outputs and workspaces made here are allocated for that stream.
+stream; outputs and workspaces made here are allocated for that stream.  All but
+latent_prefill go through the module _fast_latent (csrc/kda_latent_torch.cpp) where
+the device is the current one and no stream is named; it answers None to every call
+that it does not take or would have to refuse, which is then checked here, and made or
+refused.
 """
 from __future__ import annotations
 
@@ -32,6 +36,11 @@ import torch
 from . import _abi
 from . import _abi_latent as _an
 from .layer import _DTYPES, _on, _raw_stream
+
+try:
+    from . import _fast_latent
+except ImportError:  # not built: every call is checked and made here
+    _fast_latent = None
 
 
 def _tensor(t, name, shape, dtype, dev):
@@ -198,6 +207,10 @@ def latent_workspace_bytes(T: int, H: int, latent_dim: int, rope_dim: int, n_seq
 
 
 def _attend(what, q, cache, block_table, seq_lens, cu_seqlens, latent_dim, scale, out, workspace, stream):
+    if _fast_latent is not None and stream is None:
+        done = _fast_latent.latent_attend(q, cache, block_table, seq_lens, cu_seqlens, latent_dim, scale, out, workspace)
+        if done is not None:
+            return done
     dev, dt = _common(what, q, "q", 3)
     T, H, W = q.shape
     N, MP, tp, lp = _tables(block_table, seq_lens, dev)
@@ -302,6 +315,11 @@ def latent_append(cache: torch.Tensor, latent: torch.Tensor, k_pe: torch.Tensor,
     token stands at, and of rows_out outside every sequence, are left as they were.
     No position twice: a page that stands twice in the table of a call that writes
     both places is left with either's rows, mixed."""
+    if _fast_latent is not None and stream is None:
+        done = _fast_latent.latent_append(cache, latent, k_pe, block_table, seq_lens, cu_seqlens, weight, eps,
+                                          frequencies, interleaved, magnitude, rows_out)
+        if done is not None:
+            return done
     dev, dt = _common("latent_append", latent, "latent", 2)
     T, dc = latent.shape
     P, page, W, cp, cps, crs = _pages(cache, dev, dt)
@@ -339,6 +357,10 @@ def rotary(x: torch.Tensor, positions: torch.Tensor, frequencies: torch.Tensor, 
     [dim / 2] (rotary_frequencies).  out may be x itself, or a slice of another
     buffer (the positional part of the absorbed queries).  Angles are formed in
     fp64: far positions lose nothing."""
+    if _fast_latent is not None and stream is None:
+        done = _fast_latent.rotary(x, positions, frequencies, interleaved, magnitude, out)
+        if done is not None:
+            return done
     dev, dt = _common("rotary", x, "x", 3)
     T, H, dim = x.shape
     xp, xs, xh = _heads(x, "x", (T, H, dim), dt, dev)
