@@ -17,7 +17,7 @@ from .latent import (  # noqa: F401
     latent_append,
     latent_decode,
     latent_extend,
-    latent_prefill,
+    latent_prefill, latent_prefill_workspace_bytes,
     latent_workspace_bytes,
     rotary,
     rotary_frequencies,

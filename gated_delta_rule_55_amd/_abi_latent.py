@@ -52,7 +52,11 @@ def lib():
         L.kda_latent_workspace_bytes.restype = ctypes.c_size_t
         L.kda_latent_attend.argtypes = [ctypes.POINTER(LatentAttendDesc), ctypes.c_void_p, ctypes.c_size_t,
                                         ctypes.c_void_p]
-        L.kda_latent_prefill.argtypes = [ctypes.POINTER(LatentPrefillDesc), ctypes.c_void_p]
+        L.kda_latent_prefill_workspace_bytes.argtypes = [ctypes.POINTER(LatentPrefillDesc),
+                                                         ctypes.POINTER(ctypes.c_int)]
+        L.kda_latent_prefill_workspace_bytes.restype = ctypes.c_size_t
+        L.kda_latent_prefill.argtypes = [ctypes.POINTER(LatentPrefillDesc), ctypes.c_void_p, ctypes.c_size_t,
+                                         ctypes.c_void_p]
         L.kda_latent_append.argtypes = [ctypes.POINTER(LatentAppendDesc), ctypes.c_void_p]
         L.kda_rotary.argtypes = [ctypes.POINTER(RotaryDesc), ctypes.c_void_p]
         for name in ("kda_latent_attend", "kda_latent_prefill", "kda_latent_append", "kda_rotary"):
@@ -66,9 +70,17 @@ def make(cls, **kw):
     return cls(struct_size=ctypes.sizeof(cls), **kw)
 
 
-def latent_workspace_bytes(desc: LatentAttendDesc) -> int:
+def _workspace_bytes(name, desc) -> int:
     st = ctypes.c_int(0)
-    n = lib().kda_latent_workspace_bytes(ctypes.byref(desc), ctypes.byref(st))
+    n = getattr(lib(), name)(ctypes.byref(desc), ctypes.byref(st))
     if st.value != _abi.KDA_OK:
-        raise _abi.KdaError(st.value, "kda_latent_workspace_bytes")
+        raise _abi.KdaError(st.value, name)
     return int(n)
+
+
+def latent_workspace_bytes(desc: LatentAttendDesc) -> int:
+    return _workspace_bytes("kda_latent_workspace_bytes", desc)
+
+
+def latent_prefill_workspace_bytes(desc: LatentPrefillDesc) -> int:
+    return _workspace_bytes("kda_latent_prefill_workspace_bytes", desc)

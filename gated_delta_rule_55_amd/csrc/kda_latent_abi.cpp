@@ -133,11 +133,8 @@ int check_attend(const kda_latent_attend_desc* d, kda::LatentAttendArgs* a) {
   return KDA_OK;
 }
 
-}  // namespace
-
-extern "C" {
-
-int kda_latent_prefill(const kda_latent_prefill_desc* d, void* stream) {
+// What depends on sizes alone.
+int check_prefill(const kda_latent_prefill_desc* d, kda::LatentPrefillArgs* a) {
   if (!d) return KDA_ERR_NULL;
   if (d->struct_size != sizeof(kda_latent_prefill_desc)) return KDA_ERR_VERSION;
   if (!dtype_ok(d->dtype)) return KDA_ERR_DTYPE;
@@ -148,14 +145,45 @@ int kda_latent_prefill(const kda_latent_prefill_desc* d, void* stream) {
   const int64_t T = d->q_total, K = d->k_total, H = d->n_heads, N = d->n_seqs;
   const int64_t dn = d->dn, dr = d->dr, dv = d->dv, es = d->dtype == KDA_DTYPE_BF16 ? 2 : 4;
   if (kda::latent_query_blocks(T, N) * H >= kMaxBlocks || (!d->cu_seqlens_k && K != T)) return KDA_ERR_SHAPE;
-  kda::LatentPrefillArgs a{};
   int st;
-  if ((st = check_stride(d->q_stride, H * (dn + dr), es, &a.q_stride)) != KDA_OK ||
-      (st = check_head_strides(d->k_stride, d->k_head_stride, H, dn, es, &a.k_stride, &a.k_head)) != KDA_OK ||
-      (st = check_stride(d->k_pe_stride, dr, es, &a.pe_stride)) != KDA_OK ||
-      (st = check_head_strides(d->v_stride, d->v_head_stride, H, dv, es, &a.v_stride, &a.v_head)) != KDA_OK ||
-      (st = check_stride(d->o_stride, H * dv, es, &a.o_stride)) != KDA_OK)
+  if ((st = check_stride(d->q_stride, H * (dn + dr), es, &a->q_stride)) != KDA_OK ||
+      (st = check_head_strides(d->k_stride, d->k_head_stride, H, dn, es, &a->k_stride, &a->k_head)) != KDA_OK ||
+      (st = check_stride(d->k_pe_stride, dr, es, &a->pe_stride)) != KDA_OK ||
+      (st = check_head_strides(d->v_stride, d->v_head_stride, H, dv, es, &a->v_stride, &a->v_head)) != KDA_OK ||
+      (st = check_stride(d->o_stride, H * dv, es, &a->o_stride)) != KDA_OK)
     return st;
+  if (a->k_stride > kMaxRowStride || a->pe_stride > kMaxRowStride || a->v_stride > kMaxRowStride ||
+      a->o_stride > kMaxRowStride)
+    return KDA_ERR_SHAPE;
+  a->bf16 = d->dtype == KDA_DTYPE_BF16;
+  a->n_seqs = d->n_seqs;
+  a->n_heads = d->n_heads;
+  a->dn = d->dn;
+  a->dr = d->dr;
+  a->dv = d->dv;
+  a->q_total = (int)T;
+  a->k_total = (int)K;
+  a->scale = d->scale != 0.f ? d->scale : 1.0f / std::sqrt((float)(dn + dr));
+  return KDA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t kda_latent_prefill_workspace_bytes(const kda_latent_prefill_desc* d, int* status) {
+  kda::LatentPrefillArgs a{};
+  const int st = check_prefill(d, &a);
+  if (status) *status = st;
+  return st == KDA_OK ? kda::latent_prefill_workspace_bytes(a) : 0;
+}
+
+int kda_latent_prefill(const kda_latent_prefill_desc* d, void* workspace, size_t workspace_bytes, void* stream) {
+  kda::LatentPrefillArgs a{};
+  const int st = check_prefill(d, &a);
+  if (st != KDA_OK) return st;
+  const int64_t T = d->q_total, K = d->k_total, H = d->n_heads, N = d->n_seqs;
+  const int64_t dn = d->dn, dr = d->dr, dv = d->dv, es = a.bf16 ? 2 : 4;
   if ((!d->cu_seqlens || (d->cu_seqlens_k && !d->cu_seqlens)) && N != 1) return KDA_ERR_NULL;
   if (T > 0 && (!d->q || !d->o)) return KDA_ERR_NULL;
   if (T > 0 && K > 0 && (!d->k || !d->k_pe || !d->v)) return KDA_ERR_NULL;
@@ -163,27 +191,21 @@ int kda_latent_prefill(const kda_latent_prefill_desc* d, void* stream) {
   for (const void* p : p16)
     if (!aligned(p, 16)) return KDA_ERR_ALIGN;
   if (!aligned(d->cu_seqlens, 4) || !aligned(d->cu_seqlens_k, 4)) return KDA_ERR_ALIGN;
-  if (a.k_stride > kMaxRowStride || a.pe_stride > kMaxRowStride || a.v_stride > kMaxRowStride ||
-      a.o_stride > kMaxRowStride)
-    return KDA_ERR_SHAPE;
+  const size_t need = kda::latent_prefill_workspace_bytes(a);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return KDA_ERR_WORKSPACE;
+  if (need > 0 && !aligned(workspace, 256)) return KDA_ERR_ALIGN;
+  const Range rw = range_of(workspace, (int64_t)need);
   const RowSet o = row_set(d->o, T, a.o_stride, H * dv, es);
   const RowSet ins[] = {row_set(d->q, T, a.q_stride, H * (dn + dr), es),
                         head_rows(d->k, K, a.k_stride, H, a.k_head, dn, es), row_set(d->k_pe, K, a.pe_stride, dr, es),
                         head_rows(d->v, K, a.v_stride, H, a.v_head, dv, es)};
   for (const RowSet& r : ins)
-    if (overlap(o, r)) return KDA_ERR_ALIAS;
-  if (overlap(range_of(o), range_of(d->cu_seqlens, d->cu_seqlens ? (N + 1) * 4 : 0)) ||
-      overlap(range_of(o), range_of(d->cu_seqlens_k, d->cu_seqlens_k ? (N + 1) * 4 : 0)))
-    return KDA_ERR_ALIAS;
-  a.bf16 = d->dtype == KDA_DTYPE_BF16;
-  a.n_seqs = d->n_seqs;
-  a.n_heads = d->n_heads;
-  a.dn = d->dn;
-  a.dr = d->dr;
-  a.dv = d->dv;
-  a.q_total = (int)T;
-  a.k_total = (int)K;
-  a.scale = d->scale != 0.f ? d->scale : 1.0f / std::sqrt((float)(dn + dr));
+    if (overlap(o, r) || overlap(rw, range_of(r))) return KDA_ERR_ALIAS;
+  const Range tables[] = {range_of(d->cu_seqlens, d->cu_seqlens ? (N + 1) * 4 : 0),
+                          range_of(d->cu_seqlens_k, d->cu_seqlens_k ? (N + 1) * 4 : 0)};
+  for (const Range& r : tables)
+    if (overlap(range_of(o), r) || overlap(rw, r)) return KDA_ERR_ALIAS;
+  if (overlap(rw, range_of(o))) return KDA_ERR_ALIAS;
   a.q = d->q;
   a.k = d->k;
   a.pe = d->k_pe;
@@ -191,7 +213,7 @@ int kda_latent_prefill(const kda_latent_prefill_desc* d, void* stream) {
   a.o = d->o;
   a.cu = d->cu_seqlens;
   a.cu_k = d->cu_seqlens_k;
-  return kda::hip_status(kda::launch_latent_prefill(a, (hipStream_t)stream));
+  return kda::hip_status(kda::launch_latent_prefill(a, workspace, (hipStream_t)stream));
 }
 
 size_t kda_latent_workspace_bytes(const kda_latent_attend_desc* d, int* status) {

@@ -74,7 +74,8 @@ struct RotaryArgs {
 // in n_seqs sequences has at most.
 constexpr int kLatentQueryBlock = 128;
 inline int64_t latent_query_blocks(int64_t q_total, int64_t n_seqs) { return q_total / kLatentQueryBlock + n_seqs; }
-hipError_t launch_latent_prefill(const LatentPrefillArgs& a, hipStream_t stream);
+size_t latent_prefill_workspace_bytes(const LatentPrefillArgs& a);
+hipError_t launch_latent_prefill(const LatentPrefillArgs& a, void* workspace, hipStream_t stream);
 
 size_t latent_workspace_bytes(const LatentAttendArgs& a);
 hipError_t launch_latent_attend(const LatentAttendArgs& a, void* workspace, hipStream_t stream);

@@ -7,6 +7,8 @@
 // a query per lane), the running maximum m and sum l of the softmax in fp32, and
 // O^T += V^T P^T with the weights straight from the score registers.  O is scaled
 // by 2^(m_old - m_new) where a maximum grew.
+#include <algorithm>
+
 #include "kda_enqueue.h"
 #include "kda_latent_launch.h"
 #include "kda_latent_ops.h"
@@ -15,6 +17,29 @@ namespace kda {
 namespace {
 
 constexpr int QB = kLatentQueryBlock, KB = 64, THREADS = 256;
+
+// Where the blocks are too few for the GPU, a block's tiles go to up to `parts`
+// workgroups in equal shares; each leaves its unnormalised sums, its maxima and its
+// sums of weights in the workspace, and latent_prefill_join_kernel adds them up.
+// Measured, alone and shared (16 heads of 128 + 64, us): bf16, 256 queries on 8,192 keys
+// 198 and 50, 1,000 on 16,000 376 and 193, 128 on 1,024 33 and 20, 512 on 512 22 and 23;
+// fp32, 64 on 4,096 692 and 63.
+constexpr int PART_TILES = 2;  // of a share, if it is not all (128 queries on 1,024 keys: 1 24 us, 2 and 4 20)
+struct Parts {
+  int parts;
+  float* sums;    // [parts][q_total][H][dv]
+  float2* stats;  // [parts][q_total][H]: maximum (of scores), sum of weights
+  __host__ __device__ __forceinline__ int share(int tiles) const {
+    const int by = min(parts, max(tiles / PART_TILES, 1));
+    return (tiles + by - 1) / by;
+  }
+};
+
+int parts_of(const LatentPrefillArgs& a) {
+  // workgroups that run at a time: tiles leave room for two per CU in bf16, one in fp32
+  const int64_t slots = a.bf16 ? 512 : 256, blocks = latent_query_blocks(a.q_total, a.n_seqs) * a.n_heads;
+  return (int)std::max(std::min(slots / blocks, ((int64_t)a.k_total + KB - 1) / KB / PART_TILES), (int64_t)1);
+}
 
 // Keys, positional parts and values of a tile, each in whole column blocks.
 template <typename T, int DN, int DR, int DV>
@@ -139,8 +164,8 @@ struct Prefill {
 // Queries first .. first + QB - 1 of a sequence, of one head: its queries begin at q0, its
 // keys at k0.
 template <typename T, int DN, int DR, int DV, bool SAFE>
-__device__ __forceinline__ bool prefill_block(const LatentPrefillArgs& a, char* even, char* odd, int head, int first,
-                                              int q0, int queries, int k0, int keys) {
+__device__ __forceinline__ bool prefill_block(const LatentPrefillArgs& a, const Parts& split, char* even, char* odd,
+                                              int head, int first, int q0, int queries, int k0, int keys, int part) {
   using P = Prefill<T, DN, DR, DV>;
   using L = Tile<T, DN, DR, DV>;
   constexpr int ES = sizeof(T);
@@ -195,9 +220,11 @@ __device__ __forceinline__ bool prefill_block(const LatentPrefillArgs& a, char* 
     else if (t * KB <= wave_last + 31)
       s.template step<true, SAFE>(tile, t * KB, last, c, lane);
   };
-  const int tiles = end > 0 ? (end + KB - 1) / KB : 0;
-  if (tiles > 0) fetch(0, even);
-  for (int t = 0; t < tiles; t += 2) {
+  const int all = end > 0 ? (end + KB - 1) / KB : 0, share = split.share(all);
+  const int begin = part * share, tiles = min(begin + share, all);
+  if (part > 0 && begin >= all) return true;
+  if (begin < tiles) fetch(begin, even);
+  for (int t = begin; t < tiles; t += 2) {
     fetched();
     if (t + 1 < tiles) fetch(t + 1, odd);
     work(t, even);
@@ -218,6 +245,22 @@ __device__ __forceinline__ bool prefill_block(const LatentPrefillArgs& a, char* 
     if (any) return false;
   }
   const float sum = s.l + other_half(s.l);
+  if (share < all) {
+    const int64_t place = ((int64_t)part * a.q_total + q0 + first) * a.n_heads + head;
+    const auto sums = make_rsrc(split.sums + place * DV, INT32_MAX), stats = make_rsrc(split.stats + place, INT32_MAX);
+    const int row = (mine - first) * a.n_heads;  // (few heads: below 2^16)
+#pragma unroll
+    for (int d = 0; d < P::NV; ++d)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const f32x4 y = {s.o[d][4 * g], s.o[d][4 * g + 1], s.o[d][4 * g + 2], s.o[d][4 * g + 3]};
+        store4(y, sums, mine < queries ? (row * DV + 32 * d + 8 * g + 4 * h) * 4 : kBufferOff);
+      }
+    const u32x2 st = {__float_as_uint(s.m), __float_as_uint(sum)};
+    __builtin_amdgcn_raw_buffer_store_b64(st, stats, mine < queries && h == 0 ? row * 8 : kBufferOff, 0, 0);
+    end_of_variant<SAFE>();
+    return true;
+  }
   const float inv = last >= 0 ? __builtin_amdgcn_rcpf(sum) : 0.f;  // no key: O is 0
   const auto out = make_rsrc(static_cast<char*>(a.o) + ((int64_t)(q0 + first) * a.o_stride + head * DV) * ES, INT32_MAX);
   const int at = (int)((mine - first) * a.o_stride + 4 * h) * ES;
@@ -235,13 +278,15 @@ __device__ __forceinline__ bool prefill_block(const LatentPrefillArgs& a, char* 
 }
 
 template <typename T, int DN, int DR, int DV>
-__global__ __launch_bounds__(THREADS, sizeof(T) == 2 ? 2 : 1) void latent_prefill_kernel(LatentPrefillArgs a, int blocks, int classes) {
+__global__ __launch_bounds__(THREADS, sizeof(T) == 2 ? 2 : 1) void latent_prefill_kernel(LatentPrefillArgs a, Parts split,
+                                                                                           int blocks, int classes) {
   using L = Tile<T, DN, DR, DV>;
   __shared__ __attribute__((aligned(128))) char even[L::bytes], odd[L::bytes];
   // Workgroups go round the 8 XCDs; those of one XCD take the heads of one class, a
   // head after the other, so that the workgroups that run together there read the
   // same keys through its L2.  Late queries, which see most keys, go first.
-  const int xcd = blockIdx.x & 7, per = 8 / classes, i = blockIdx.x >> 3;
+  const int xcd = blockIdx.x & 7, per = 8 / classes, part = (blockIdx.x >> 3) % split.parts;
+  const int i = (blockIdx.x >> 3) / split.parts;
   const int nb = (blocks + per - 1) / per;
   const int head = xcd / per + classes * (i / nb);
   const int back = xcd % per + per * (i % nb);
@@ -254,40 +299,91 @@ __global__ __launch_bounds__(THREADS, sizeof(T) == 2 ? 2 : 1) void latent_prefil
   const int32_t* cu_k = a.cu_k ? a.cu_k : a.cu;
   const int k0 = cu_k ? seq_start(cu_k, n, a.k_total) : 0, k1 = cu_k ? seq_start(cu_k, n + 1, a.k_total) : a.k_total;
   const int first = (int)block * QB, keys = max(k1 - k0, 0);
-  if (!prefill_block<T, DN, DR, DV, false>(a, even, odd, head, first, q0, q1 - q0, k0, keys))
-    prefill_block<T, DN, DR, DV, true>(a, even, odd, head, first, q0, q1 - q0, k0, keys);
+  if (!prefill_block<T, DN, DR, DV, false>(a, split, even, odd, head, first, q0, q1 - q0, k0, keys, part))
+    prefill_block<T, DN, DR, DV, true>(a, split, even, odd, head, first, q0, q1 - q0, k0, keys, part);
+}
+
+// The rows of blocks that were shared: a workgroup takes some heads of a token, DV / 4
+// threads a row, and brings the parts' sums to the largest maximum.
+template <typename T, int DV>
+__global__ __launch_bounds__(THREADS) void latent_prefill_join_kernel(LatentPrefillArgs a, Parts split, int groups) {
+  constexpr int WIDTH = DV / 4, HEADS = THREADS / WIDTH;
+  const int t = blockIdx.x / groups, head = blockIdx.x % groups * HEADS + threadIdx.x / WIDTH;
+  const int at = 4 * (threadIdx.x % WIDTH);
+  const int n = a.cu ? find_last(a.n_seqs, [&](int i) { return seq_start(a.cu, i, a.q_total) <= t; }) : 0;
+  const int q0 = a.cu ? seq_start(a.cu, n, a.q_total) : 0, q1 = a.cu ? seq_start(a.cu, n + 1, a.q_total) : a.q_total;
+  if (t < q0 || t >= q1 || head >= a.n_heads) return;
+  const int32_t* cu_k = a.cu_k ? a.cu_k : a.cu;
+  const int k0 = cu_k ? seq_start(cu_k, n, a.k_total) : 0, k1 = cu_k ? seq_start(cu_k, n + 1, a.k_total) : a.k_total;
+  const int past = max(k1 - k0, 0) - (q1 - q0);
+  const int end = min((t - q0) / QB * QB + QB, q1 - q0) + past;
+  const int all = end > 0 ? (end + KB - 1) / KB : 0, share = split.share(all);
+  if (share >= all) return;
+  const int parts = (all + share - 1) / share;
+  const float c = a.scale * kLog2e;
+  const int64_t place = (int64_t)t * a.n_heads + head, step = (int64_t)a.q_total * a.n_heads;
+  float m = -__builtin_inff(), l = 0.f;
+  f32x4 o = zero4();
+#pragma unroll 4
+  for (int p = 0; p < parts; ++p) {
+    const float2 st = split.stats[place + p * step];
+    const f32x4 x = *reinterpret_cast<const f32x4*>(split.sums + (place + p * step) * DV + at);
+    const float top = fmaxf(m, st.x), base = top == -__builtin_inff() ? 0.f : __fmul_rn(top, c);
+    const float before = fast_exp2(__fmul_rn(m, c) - base), now = fast_exp2(__fmul_rn(st.x, c) - base);
+    m = top;
+    l = l * before + st.y * now;
+    o = o * before + x * now;
+  }
+  const float inv = t - q0 + past >= 0 ? 1.f / l : 0.f;  // no key: O is 0
+  typename Vec4<T>::type y;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) y[e] = from_f32<T>(o[e] * inv);
+  *reinterpret_cast<typename Vec4<T>::type*>(static_cast<T*>(a.o) + (int64_t)t * a.o_stride + head * DV + at) = y;
 }
 
 template <typename T, int DN, int DR, int DV>
-hipError_t run(const LatentPrefillArgs& a, hipStream_t stream) {
+hipError_t run(const LatentPrefillArgs& a, const Parts& split, hipStream_t stream) {
   const int64_t blocks = latent_query_blocks(a.q_total, a.n_seqs);
   int classes = 1;  // of heads: the XCDs share them evenly
   while (classes < 8 && a.n_heads % (2 * classes) == 0) classes *= 2;
   const int64_t per = 8 / classes;
-  const int64_t grid = 8 * ((blocks + per - 1) / per) * (a.n_heads / classes);
-  return enqueue(latent_prefill_kernel<T, DN, DR, DV>, (unsigned)grid, THREADS, stream, a, (int)blocks, classes);
+  const int64_t grid = 8 * ((blocks + per - 1) / per) * (a.n_heads / classes) * split.parts;
+  const hipError_t e =
+      enqueue(latent_prefill_kernel<T, DN, DR, DV>, (unsigned)grid, THREADS, stream, a, split, (int)blocks, classes);
+  if (e != hipSuccess || split.parts == 1) return e;
+  const int groups = (a.n_heads + THREADS / (DV / 4) - 1) / (THREADS / (DV / 4));
+  return enqueue(latent_prefill_join_kernel<T, DV>, (unsigned)(a.q_total * groups), THREADS, stream, a, split, groups);
 }
 
 template <typename T, int DN, int DR>
-hipError_t by_dv(const LatentPrefillArgs& a, hipStream_t stream) {
-  return a.dv == 128 ? run<T, DN, DR, 128>(a, stream) : run<T, DN, DR, 64>(a, stream);
+hipError_t by_dv(const LatentPrefillArgs& a, const Parts& s, hipStream_t stream) {
+  return a.dv == 128 ? run<T, DN, DR, 128>(a, s, stream) : run<T, DN, DR, 64>(a, s, stream);
 }
 
 template <typename T, int DN>
-hipError_t by_dr(const LatentPrefillArgs& a, hipStream_t stream) {
-  return a.dr == 64 ? by_dv<T, DN, 64>(a, stream) : by_dv<T, DN, 32>(a, stream);
+hipError_t by_dr(const LatentPrefillArgs& a, const Parts& s, hipStream_t stream) {
+  return a.dr == 64 ? by_dv<T, DN, 64>(a, s, stream) : by_dv<T, DN, 32>(a, s, stream);
 }
 
 template <typename T>
-hipError_t by_dn(const LatentPrefillArgs& a, hipStream_t stream) {
-  return a.dn == 128 ? by_dr<T, 128>(a, stream) : by_dr<T, 64>(a, stream);
+hipError_t by_dn(const LatentPrefillArgs& a, const Parts& s, hipStream_t stream) {
+  return a.dn == 128 ? by_dr<T, 128>(a, s, stream) : by_dr<T, 64>(a, s, stream);
 }
+
+int64_t sums_bytes(const LatentPrefillArgs& a, int parts) { return (int64_t)parts * a.q_total * a.n_heads * a.dv * 4; }
 
 }  // namespace
 
-hipError_t launch_latent_prefill(const LatentPrefillArgs& a, hipStream_t stream) {
+size_t latent_prefill_workspace_bytes(const LatentPrefillArgs& a) {
+  const int parts = a.q_total == 0 ? 1 : parts_of(a);
+  return parts == 1 ? 0 : (size_t)(sums_bytes(a, parts) + (int64_t)parts * a.q_total * a.n_heads * 8);
+}
+
+hipError_t launch_latent_prefill(const LatentPrefillArgs& a, void* workspace, hipStream_t stream) {
   if (a.q_total == 0) return hipSuccess;
-  return a.bf16 ? by_dn<bf16>(a, stream) : by_dn<float>(a, stream);
+  Parts s = {parts_of(a), static_cast<float*>(workspace), nullptr};
+  if (s.parts > 1) s.stats = reinterpret_cast<float2*>(static_cast<char*>(workspace) + sums_bytes(a, s.parts));
+  return a.bf16 ? by_dn<bf16>(a, s, stream) : by_dn<float>(a, s, stream);
 }
 
 }  // namespace kda

@@ -122,9 +122,30 @@ def _cu(cu, name, dev):
     return cu.shape[0] - 1, _dense(cu, name, cu.shape, torch.int32, dev)
 
 
+def _workspace(given, need, dev):
+    """Address and bytes of a call's workspace, and the tensor that holds it."""
+    if given is None:
+        n = need()
+        if n == 0:
+            return None, 0, None
+        given = torch.empty(n, dtype=torch.uint8, device=dev)
+    elif not isinstance(given, torch.Tensor) or given.device != dev or not given.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+    return given.data_ptr(), given.numel() * given.element_size(), given
+
+
+def latent_prefill_workspace_bytes(T: int, K: int, H: int, nope_dim: int, rope_dim: int, value_dim: int,
+                                   n_seqs: int = 1, dtype: torch.dtype = torch.bfloat16) -> int:
+    """Bytes of workspace latent_prefill needs for T queries and K keys in n_seqs sequences."""
+    return _an.latent_prefill_workspace_bytes(_an.make(
+        _an.LatentPrefillDesc, dtype=_DTYPES[dtype], n_seqs=n_seqs, n_heads=H, dn=nope_dim, dr=rope_dim,
+        dv=value_dim, q_total=T, k_total=K, cu_seqlens_k=None if T == K else 16))
+
+
 def latent_prefill(q: torch.Tensor, k: torch.Tensor, k_pe: torch.Tensor, v: torch.Tensor,
                    cu_seqlens: Optional[torch.Tensor] = None, cu_seqlens_k: Optional[torch.Tensor] = None,
-                   scale: Optional[float] = None, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+                   scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                   workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Causal attention over packed prompts on expanded keys and values:
     o_i = sum_j softmax_j(scale (q_i[:dn] . k_j + q_i[dn:] . k_pe_j)) v_j.
 
@@ -140,7 +161,8 @@ def latent_prefill(q: torch.Tensor, k: torch.Tensor, k_pe: torch.Tensor, v: torc
     slices of one buffer [K, H, dn + dv], k_pe of wider rows; strides are multiples
     of 16 bytes.  cu_seqlens and cu_seqlens_k are read on the device: contents that
     do not ascend from 0 give unspecified results but no access out of bounds.
-    Rows of out outside every sequence are left as they were."""
+    Rows of out outside every sequence are left as they were.  workspace: a buffer of
+    latent_prefill_workspace_bytes bytes (often 0), as in latent_decode."""
     dev, dt = _common("latent_prefill", q, "q", 3)
     for t, name in ((k, "k"), (v, "v")):
         if not isinstance(t, torch.Tensor) or t.dim() != 3:
@@ -169,7 +191,8 @@ def latent_prefill(q: torch.Tensor, k: torch.Tensor, k_pe: torch.Tensor, v: torc
             ctypes.sizeof(_an.LatentPrefillDesc), _DTYPES[dt], N, H, dn, dr, dv,
             0.0 if scale is None else _positive(scale), T, K, qp, kp, pp, vp, op, qs, ks, kh, ps, vs, vh, os_,
             cup, cukp)
-        st = _an.lib().kda_latent_prefill(ctypes.byref(desc), _raw_stream(dev))
+        wp, wn, workspace = _workspace(workspace, lambda: _an.latent_prefill_workspace_bytes(desc), dev)
+        st = _an.lib().kda_latent_prefill(ctypes.byref(desc), wp, wn, _raw_stream(dev))
     if st != _abi.KDA_OK:
         raise _abi.KdaError(st, "kda_latent_prefill")
     return out
@@ -230,14 +253,7 @@ def _attend(what, q, cache, block_table, seq_lens, cu_seqlens, latent_dim, scale
         desc = _an.LatentAttendDesc(
             ctypes.sizeof(_an.LatentAttendDesc), _DTYPES[dt], N, H, latent_dim, W - latent_dim, page, MP, P,
             _positive(scale), T, qp, cp, op, qs, cps, crs, os_, tp, lp, cup)
-        if workspace is None:
-            need = _an.latent_workspace_bytes(desc)
-            if need:
-                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        elif workspace.device != dev or not workspace.is_contiguous():
-            raise ValueError(f"workspace must be a contiguous tensor on {dev}")
-        wp, wn = (None, 0) if workspace is None else (
-            workspace.data_ptr(), workspace.numel() * workspace.element_size())
+        wp, wn, workspace = _workspace(workspace, lambda: _an.latent_workspace_bytes(desc), dev)
         st = _an.lib().kda_latent_attend(ctypes.byref(desc), wp, wn, _raw_stream(dev))
     if st != _abi.KDA_OK:
         raise _abi.KdaError(st, "kda_latent_attend")

@@ -80,7 +80,15 @@ typedef struct {
   const int32_t* cu_seqlens_k; /* device or NULL                                */
 } kda_latent_prefill_desc;
 
-int kda_latent_prefill(const kda_latent_prefill_desc* d, void* stream);
+/* Bytes of device workspace kda_latent_prefill needs: 0 but where the blocks of
+ * queries are too few for the GPU and their keys are shared out (depends on sizes
+ * only: dtype, n_seqs, n_heads, dn, dr, dv, q_total and k_total).  *status (host, may
+ * be NULL) receives the kda_status of the check; 0 is returned when it fails. */
+size_t kda_latent_prefill_workspace_bytes(const kda_latent_prefill_desc* d, int* status);
+
+/* workspace: as in kda_latent_attend. */
+int kda_latent_prefill(const kda_latent_prefill_desc* d, void* workspace, size_t workspace_bytes,
+                       void* stream);
 
 /* Absorbed attention of new tokens over the paged cache, which holds their own
  * rows already: new token i of a sequence's Lq sees positions
