@@ -1,18 +1,30 @@
 // kda_latent_attend.hip -- absorbed latent attention over a paged cache
 // (kda_latent_attend): new tokens' queries of all heads against the cached rows
-// [c | k_pe] themselves, o = sum_j p_j c_j.
+// [c | k_pe] themselves, o = sum_j p_j c_j, p the softmax of scale q . row_j.
 //
 // All heads share the rows, so a row of queries is a (token, head) pair and a
-// workgroup takes 32 of a sequence's (a unit).  It walks the rows of the cache in
-// tiles of 64 through LDS, where a tile is keys and values at once.  Four waves
-// share a tile's work: for the scores S^T = C Q^T each takes 16 keys (and keeps all
-// its queries' fragments in registers), for O^T += C^T P^T a quarter of the dc
-// columns; the weights P and the maxima are exchanged through LDS.
+// workgroup takes R = 32 or 64 of a sequence's (a unit).  It walks the rows of the
+// cache in tiles (bf16 64 rows, fp32 32) through LDS, where a tile is keys and values
+// at once; two tiles, one worked on while the other is fetched straight into LDS, fill
+// it, so a CU has one workgroup (bf16 eight waves, fp32 four).  Waves share a tile's
+// work: for the scores S^T = C Q^T they are R / 16 groups of queries, whose
+// fragments they keep in registers, times groups of keys; for O^T += C^T P^T each
+// has its share of the dc columns, in registers from the first tile to the last.  The
+// maxima and the weights P are exchanged through LDS; running maxima and sums are
+// fp32, and O is scaled only by tiles that raise a maximum.
 //
 // The tiles of all units together are cut into equal runs, one per workgroup, so
 // that a long sequence is read by many.  A unit that is cut leaves its pieces
 // (unnormalised sums, maximum, sum of weights, fp32) in the workspace and
 // latent_join_kernel adds them up.
+//
+// What bounds it (512 + 64, bf16).  Few heads: the rows' bytes; 64 sequences of 8,192
+// rows, 16 heads, 137 us, 4.4 TB/s of the 5.0 that a copy reaches.  Many queries a row:
+// a tile's turn takes 2.9 us at R = 64, of which the matrix instructions are 0.9, the
+// reads of LDS (each key by four waves) 1.4, and three barriers keep the two from
+// overlapping fully: 2,048 new tokens of 32 heads 3.1 ms, 0.80 PFLOP/s.  One
+// sequence: the start (tables, pages and first rows one after the other: 7 us), the end
+// of a piece (2 us) and the join.
 #include "kda_enqueue.h"
 #include "kda_latent_launch.h"
 #include "kda_latent_ops.h"
@@ -23,17 +35,28 @@ namespace {
 constexpr int JOIN_THREADS = 256;
 constexpr int RUNS = 256;     // workgroups: their tiles in LDS leave room for one per CU
 // What it costs to begin a unit's piece (its queries, the first rows' latency) and to end
-// it, in tiles: each unit counts as that many more, in front, so that a run that crosses
-// from one into another has fewer tiles for it.
-constexpr int SETUP = 3;
-constexpr int MIN_TILES = SETUP + 2;  // of a run (fp32, whose tiles are shorter and take longer: one less)
+// it, in tiles of KB rows (64: bf16; fp32's 32 rows take longer, 5 us: three sequences of 200
+// rows 26 us with 1, 30 with 2, 41 with 3): each unit counts as that many more, in front, so
+// that a run that crosses from one into another has fewer tiles for it.
+constexpr int setup_of(int KB) { return KB == 64 ? 3 : 1; }
+// Tiles of a run at least: one with its setup.  (Two, bf16: one sequence of 1,000 rows 27
+// us for 25; 32,768 rows 30 both ways.)
+constexpr int min_tiles(int KB) { return setup_of(KB) + 1; }
 
 // The workspace.  A run has at most two pieces of units that are cut: one that begins
 // inside its unit (place 2 run) and one that begins with it (place 2 run + 1).  The
 // latter's head says where the unit's other pieces are.  Heads are numbered by unit
-// where a call has few of them, so that the join has a workgroup for each row and 128
-// columns of these and no idle ones, else by run, with fewer workgroups each.
-constexpr int FEW_UNITS = 64;
+// where a call has few of them, so that the join has a workgroup for each row of these and
+// no idle ones (one sequence of 32,768 rows, 128 heads: 46 us, by run 69), else by run,
+// with 16 workgroups each, which idle where a run begins no unit that is cut.  Where even the
+// rows would not fill the GPU a workgroup takes 128 columns of one (32 heads: 28 us
+// for 32; at 64 units, 64 sequences of 64 heads, it would cost: 117 for 106).
+constexpr int FEW_UNITS = 64, JOIN_SHARES = 16;
+// Units are of 64 rows where that leaves a run this many tiles: each is read from LDS
+// and from memory half as often (2,048 new tokens 3.1 ms for 4.6, 24 x 4 97 us for 108, 256
+// sequences of 1,000 rows and 128 heads 166 for 225).  With fewer tiles the shorter turns of
+// 32 rows, in more runs, win (four sequences of 8,000 rows, 128 heads: 40 us for 50).
+constexpr int LONG_RUN = 6;
 struct Plan {
   int rows;  // of a unit
   bool by_unit;
@@ -42,10 +65,11 @@ struct Plan {
   size_t heads_bytes, sums_bytes, bytes;
   explicit Plan(const LatentAttendArgs& a) {
     const int64_t T = a.pages.t_total, N = a.pages.n_seqs, H = a.n_heads;
-    rows = a.bf16 && T * H >= 64 * N ? 64 : 32;
     const int tile = a.bf16 ? 64 : 32;
+    const int64_t most = ((int64_t)a.pages.max_pages * a.pages.page_size + tile - 1) / tile;  // of a sequence
+    rows = a.bf16 && T * H >= 64 * N && T * H / 64 * most >= LONG_RUN * RUNS ? 64 : 32;
     units = a.pages.cu ? T * H / rows + N : N * ((H + rows - 1) / rows);
-    const int64_t tiles = units * (SETUP + ((int64_t)a.pages.max_pages * a.pages.page_size + tile - 1) / tile) / MIN_TILES;
+    const int64_t tiles = units * (setup_of(tile) + most) / min_tiles(tile);
     runs = (int)(tiles < RUNS ? (tiles < 1 ? 1 : tiles) : RUNS);
     by_unit = units <= FEW_UNITS;
     heads = by_unit ? (int)units : runs;
@@ -67,7 +91,7 @@ struct Sequence {
   int start, tokens;        // first new token; new tokens
   int length, rows;         // seq_lens, and the rows of it that the table has places for
   int64_t units;            // of R queries
-  int tiles;                // of KB rows, of each unit, and SETUP
+  int tiles;                // of KB rows, of each unit, and its setup
   __device__ __forceinline__ int64_t all() const { return units * tiles; }
 };
 template <int R, int KB>
@@ -78,7 +102,7 @@ __device__ __forceinline__ Sequence sequence_of(const LatentPages& g, int n_head
   s.length = max(g.lens[n], 0);
   s.rows = min(s.length, g.max_pages * g.page_size);
   s.units = ((int64_t)s.tokens * n_heads + R - 1) / R;
-  s.tiles = SETUP + max((s.rows + KB - 1) / KB, 1);
+  s.tiles = setup_of(KB) + max((s.rows + KB - 1) / KB, 1);
   return s;
 }
 
@@ -107,13 +131,14 @@ __device__ __forceinline__ int64_t divide(int64_t a, int b) {
   return a >> 32 == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
-// The tiles of all units (and SETUP each), total, in `runs` equal runs: the first `longer` of them have
+// The tiles of all units (and their setups), total, in `runs` equal runs: the first `longer` of them have
 // one more than the others' `share`.
+template <int KB>
 struct Runs {
   int64_t total, share;
   int runs, longer;
   __device__ __forceinline__ Runs(int64_t all, int most) : total(all) {
-    runs = (int)min((int64_t)most, max(all / MIN_TILES, (int64_t)1));
+    runs = (int)min((int64_t)most, max(all / min_tiles(KB), (int64_t)1));
     share = divide(all, runs);
     longer = (int)(all - share * runs);
   }
@@ -450,7 +475,7 @@ __device__ __forceinline__ bool attend_piece(const LatentAttendArgs& a, const Wo
     int some = 0;
 #pragma unroll
     for (int k = 0; k < S::KG; ++k) all += x.sums[k][r], some |= x.seen[k][r];
-    if (tile0 == 0 && tile1 == s.tiles - SETUP) {
+    if (tile0 == 0 && tile1 == s.tiles - setup_of(S::KB)) {
       const int tok = (row0 + r) / a.n_heads;
       const int at = (int)((tok - tok0) * a.o_stride + (row0 + r - tok * a.n_heads) * DC + S::COLS * wave + 4 * h) * ES;
       const float inv = some ? __builtin_amdgcn_rcpf(all) : 0.f;  // no key: O is 0
@@ -500,7 +525,7 @@ __global__ __launch_bounds__((Shape<T, DC, DR, R>::THREADS), 1) void latent_atte
   int64_t mine = 0, total;
   for (int i = first; i < min(first + each, g.n_seqs); ++i) mine += sequence_of<R, KB>(g, a.n_heads, i).all();
   const int64_t upto = scan<S::NW>(mine, waves, &total);
-  const Runs runs(uniform(total), gridDim.x);
+  const Runs<KB> runs(uniform(total), gridDim.x);
   if (run >= runs.runs) return;
   const int64_t lo = runs.begin(run), hi = runs.begin(run + 1);
   if (lo >= hi) return;
@@ -525,7 +550,7 @@ __global__ __launch_bounds__((Shape<T, DC, DR, R>::THREADS), 1) void latent_atte
     const int unit = (int)divide(in_seq, s.tiles), from = (int)(in_seq - (int64_t)unit * s.tiles);
     const int to = (int)min((int64_t)s.tiles, from + (hi - pos));
     pos += to - from;
-    const Piece pc = {n, unit, max(from - SETUP, 0), max(to - SETUP, 0), run, runs.reached(run, s.tiles - to)};
+    const Piece pc = {n, unit, max(from - setup_of(KB), 0), max(to - setup_of(KB), 0), run, runs.reached(run, s.tiles - to)};
     if (pos - seq_at >= s.all()) {
       seq_at = pos;
       ++n;
@@ -610,7 +635,7 @@ hipError_t run(const LatentAttendArgs& a, const Plan& plan, const Workspace& ws,
   if (plan.units <= FEW_UNITS / 8)  // their rows alone would not fill the GPU
     return enqueue(latent_join_kernel<T, DC, R, KB, 128>, (unsigned)(plan.heads * R * (DC / 128)), JOIN_THREADS, stream, a,
                    ws, R * (DC / 128));
-  const int shares = plan.by_unit ? R : 16;
+  const int shares = plan.by_unit ? R : JOIN_SHARES;
   return enqueue(latent_join_kernel<T, DC, R, KB, DC>, (unsigned)(plan.heads * shares), JOIN_THREADS, stream, a, ws, shares);
 }
 
