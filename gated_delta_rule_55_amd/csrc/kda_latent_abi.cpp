@@ -263,6 +263,7 @@ int kda_latent_append(const kda_latent_append_desc* d, void* stream) {
   int st = check_pages(d->dtype, d->n_seqs, d->dc, d->dr, d->page_size, d->max_pages, d->n_pages, d->page_stride,
                        d->row_stride, d->t_total, d->cu_seqlens != nullptr, &g);
   if (st != KDA_OK) return st;
+  if (d->t_total / 4 >= kMaxBlocks) return KDA_ERR_SHAPE;  // a workgroup for 4 tokens
   if (d->rotary != KDA_ROTARY_HALF && d->rotary != KDA_ROTARY_INTERLEAVED) return KDA_ERR_UNSUPPORTED;
   if (!(std::isfinite(d->eps) && d->eps >= 0.f) || !std::isfinite(d->magnitude)) return KDA_ERR_SHAPE;
   const int64_t es = d->dtype == KDA_DTYPE_BF16 ? 2 : 4, W = d->dc + d->dr, T = d->t_total;

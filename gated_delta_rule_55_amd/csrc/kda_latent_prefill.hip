@@ -7,6 +7,14 @@
 // a query per lane), the running maximum m and sum l of the softmax in fp32, and
 // O^T += V^T P^T with the weights straight from the score registers.  O is scaled
 // by 2^(m_old - m_new) where a maximum grew.
+//
+// Every key is read from LDS by four waves and every tile by all workgroups of its
+// head, so it is the matrix cores, the vector unit (exponentials, maxima, sums) and
+// LDS that bound it, not the memory.  Two tiles, one worked on while the other is
+// fetched straight into LDS, take 80 KB in bf16: two workgroups a CU, so that one's
+// softmax runs beside the other's products; fp32 takes 160 KB, one.  32,768 tokens, 32
+// heads of 128 + 64, bf16: 10.8 ms, 1.0 PFLOP/s where a large matrix product reaches 1.18; matrix
+// cores busy for 52 % of the cycles (the clock is at 1.8 GHz under this load), LDS for 43 %.
 #include <algorithm>
 
 #include "kda_enqueue.h"
@@ -170,7 +178,7 @@ __device__ __forceinline__ bool prefill_block(const LatentPrefillArgs& a, const 
   using L = Tile<T, DN, DR, DV>;
   constexpr int ES = sizeof(T);
   const int lane = threadIdx.x & 63, wave = wave_index(), h = lane >> 5;
-    const int mine = first + 32 * wave + (lane & 31);
+  const int mine = first + 32 * wave + (lane & 31);
   const int last = mine + (keys - queries);                     // the last key this lane's query sees
   const int wave_last = first + 32 * wave + (keys - queries);   // the last one that all of the wave's see
   // keys that the workgroup's last query sees

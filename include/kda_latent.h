@@ -156,13 +156,13 @@ typedef enum {
 typedef struct {
   uint32_t struct_size;        /* sizeof(kda_latent_append_desc)                */
   int32_t dtype;               /* kda_dtype of latent, k_pe, cache, rows_out    */
-  int32_t n_seqs;              /* N >= 0                                        */
+  int32_t n_seqs;              /* N, 0 (nothing to do) .. 2^24                  */
   int32_t dc, dr;              /* dc 256 or 512, dr 32 or 64                    */
   int32_t page_size, max_pages, n_pages; /* as in kda_latent_attend_desc        */
   int32_t rotary;              /* kda_rotary_layout                             */
   float eps;                   /* >= 0, of the norm                             */
   float magnitude;             /* 0 = 1                                         */
-  int64_t t_total;             /* 0 .. 2^31 - 65                                */
+  int64_t t_total;             /* 0 .. 2^25 - 1                                 */
   const void* latent;
   const void* k_pe;
   void* cache;
@@ -186,7 +186,8 @@ typedef struct {
   uint32_t struct_size;        /* sizeof(kda_rotary_desc)                       */
   int32_t dtype;               /* kda_dtype of x, y                             */
   int32_t n_heads;             /* H, 1 .. 65535                                 */
-  int32_t dim;                 /* a multiple of 16, 16 .. 256                   */
+  int32_t dim;                 /* a multiple of 16, 16 .. 256;                  */
+                               /* t_total min(H, 8) dim / 4 < 2^31              */
   int32_t rotary;              /* kda_rotary_layout                             */
   float magnitude;             /* 0 = 1                                         */
   int64_t t_total;             /* 0 .. 2^31 - 65                                */

@@ -176,6 +176,7 @@ APPEND = dict(dtype=2, n_seqs=3, dc=512, dr=64, page_size=64, max_pages=8, n_pag
 @pytest.mark.parametrize("over,status", [
     (dict(struct_size=8), -8), (dict(dtype=0), -3), (dict(n_seqs=-1), -2), (dict(dc=1024), -4), (dict(dr=96), -4),
     (dict(page_size=0), -2), (dict(max_pages=-1), -2), (dict(n_pages=-1), -2), (dict(t_total=-1), -2),
+    (dict(t_total=1 << 25), -2),     # threads of a launch past 2^31
     (dict(rotary=2), -4), (dict(rotary=-1), -4), (dict(eps=-1.0), -2), (dict(eps=NAN), -2), (dict(eps=INF), -2),
     (dict(magnitude=NAN), -2), (dict(magnitude=INF), -2), (dict(cu_seqlens=None), -2),
     (dict(latent_stride=504), -2), (dict(k_pe_stride=68), -2), (dict(rows_out_stride=568), -2), (dict(row_stride=512), -2),
