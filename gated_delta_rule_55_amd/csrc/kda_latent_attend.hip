@@ -18,8 +18,8 @@
 // (unnormalised sums, maximum, sum of weights, fp32) in the workspace and
 // latent_join_kernel adds them up.
 //
-// What bounds it (512 + 64, bf16).  Few heads: the rows' bytes; 64 sequences of 8,192
-// rows, 16 heads, 137 us, 4.4 TB/s of the 5.0 that a copy reaches.  Many queries a row:
+// What bounds it (512 + 64, bf16).  One token a sequence: the rows' bytes; 64 sequences of
+// 8,192 rows on average, 32 heads, 137 us, 4.4 TB/s of the 5.0 that a copy reaches.  Many queries a row:
 // a tile's turn takes 2.9 us at R = 64, of which the matrix instructions are 0.9, the
 // reads of LDS (each key by four waves) 1.4, and three barriers keep the two from
 // overlapping fully: 2,048 new tokens of 32 heads 3.1 ms, 0.80 PFLOP/s.  One
@@ -53,7 +53,8 @@ constexpr int min_tiles(int KB) { return setup_of(KB) + 1; }
 // for 32; at 64 units, 64 sequences of 64 heads, it would cost: 117 for 106).
 constexpr int FEW_UNITS = 64, JOIN_SHARES = 16;
 // Units are of 64 rows where that leaves a run this many tiles: each is read from LDS
-// and from memory half as often (2,048 new tokens 3.1 ms for 4.6, 24 x 4 97 us for 108, 256
+// and from memory half as often (2,048 new tokens 3.1 ms for 4.6, 24 sequences of some 4
+// tokens 97 us for 108, 256
 // sequences of 1,000 rows and 128 heads 166 for 225).  With fewer tiles the shorter turns of
 // 32 rows, in more runs, win (four sequences of 8,000 rows, 128 heads: 40 us for 50).
 constexpr int LONG_RUN = 6;
