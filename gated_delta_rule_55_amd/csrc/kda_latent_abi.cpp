@@ -34,8 +34,8 @@ constexpr int64_t kMaxBlocks = (int64_t)1 << 23;
 bool dtype_ok(int32_t dtype) { return dtype == KDA_DTYPE_F32 || dtype == KDA_DTYPE_BF16; }
 bool heads_ok(int32_t n) { return n >= 1 && n <= 65535; }
 bool tokens_ok(int64_t n) { return n >= 0 && n <= kMaxTokens; }
-// A scale that fp32 holds as a normal number.
-bool scale_ok(float s) { return std::isfinite(s) && s >= FLT_MIN; }
+// A scale that fp32 holds as a normal number, times log2(e) too.
+bool scale_ok(float s) { return std::isfinite(1.5f * s) && s >= FLT_MIN; }
 
 // A stride in elements: 0 = dense; else at least `row`, a multiple of 16 bytes and at
 // most 2^28.

@@ -68,7 +68,7 @@ typedef struct {
   int32_t n_seqs;              /* N >= 1                                        */
   int32_t n_heads;             /* H, 1 .. 65535                                 */
   int32_t dn, dr, dv;          /* dn and dv 64 or 128, dr 32 or 64              */
-  float scale;                 /* > 0; 0 = (dn + dr)^-1/2                       */
+  float scale;                 /* 2^-126 .. 2^127; 0 = (dn + dr)^-1/2           */
   int64_t q_total, k_total;    /* 0 .. 2^31 - 65; (q_total / 128 + N) H < 2^23  */
   const void* q;
   const void* k;
@@ -112,7 +112,7 @@ typedef struct {
   int32_t page_size;           /* >= 1; max_pages * page_size <= 2^31 - 257     */
   int32_t max_pages;           /* >= 1: columns of block_table                  */
   int32_t n_pages;             /* >= 0                                          */
-  float scale;                 /* > 0                                           */
+  float scale;                 /* 2^-126 .. 2^127                               */
   int64_t t_total;             /* new tokens; t_total H <= 2^31 - 65            */
   const void* q;
   const void* cache;

@@ -63,7 +63,7 @@ PREFILL = dict(dtype=2, n_seqs=2, n_heads=4, dn=128, dr=64, dv=128, q_total=300,
     (dict(n_heads=65536), -2), (dict(q_total=-1), -2), (dict(k_total=-1), -2), (dict(q_total=I32 - 63), -2),
     (dict(k_total=I32 - 63), -2), (dict(q_total=1 << 30, n_heads=16), -2), (dict(n_seqs=1 << 23), -2),
     (dict(dn=96), -4), (dict(dv=32), -4), (dict(dr=128), -4), (dict(dr=0), -4),
-    (dict(scale=-1.0), -2), (dict(scale=NAN), -2), (dict(scale=INF), -2), (dict(scale=1e-40), -2),
+    (dict(scale=-1.0), -2), (dict(scale=NAN), -2), (dict(scale=INF), -2), (dict(scale=1e-40), -2), (dict(scale=3e38), -2),
     (dict(cu_seqlens_k=None), -2),   # other keys than queries
     (dict(q_stride=760), -2), (dict(q_stride=772), -2), (dict(k_stride=500), -2), (dict(k_head_stride=120), -2),
     (dict(k_head_stride=132), -2), (dict(v_stride=-8), -2), (dict(k_stride=(1 << 22) + 8), -2),
@@ -128,6 +128,7 @@ ATTEND = dict(dtype=2, n_seqs=3, n_heads=4, dc=512, dr=64, page_size=64, max_pag
     (dict(page_size=0), -2), (dict(max_pages=0), -2), (dict(n_pages=-1), -2), (dict(page_size=I32, max_pages=2), -2),
     (dict(page_size=I32 - 255, max_pages=1), -2), (dict(t_total=-1), -2), (dict(t_total=I32 // 4), -2),
     (dict(scale=0.0), -2), (dict(scale=-0.1), -2), (dict(scale=NAN), -2), (dict(scale=INF), -2), (dict(scale=1e-39), -2),
+    (dict(scale=3e38), -2),
     (dict(cu_seqlens=None), -2),     # 9 tokens of 3 sequences
     (dict(q_stride=2296), -2), (dict(q_stride=2308), -2), (dict(o_stride=2040), -2), (dict(o_stride=(1 << 22) + 8), -2),
     (dict(row_stride=568), -2), (dict(row_stride=580), -2), (dict(page_stride=64 * 576 - 8), -2),
