@@ -20,9 +20,9 @@
 //
 // What bounds it (512 + 64, bf16).  One token a sequence: the rows' bytes; 64 sequences of
 // 8,192 rows on average, 32 heads, 137 us, 4.4 TB/s of the 5.0 that a copy reaches.  Many queries a row:
-// a tile's turn takes 2.9 us at R = 64, of which the matrix instructions are 0.9, the
+// a tile's turn takes 2.8 us at R = 64, of which the matrix instructions are 0.9, the
 // reads of LDS (each key by four waves) 1.4, and three barriers keep the two from
-// overlapping fully: 2,048 new tokens of 32 heads 3.1 ms, 0.80 PFLOP/s.  One
+// overlapping fully: 2,048 new tokens of 32 heads 3.0 ms, 0.82 PFLOP/s.  One
 // sequence: the start (tables, pages and first rows one after the other: 7 us), the end
 // of a piece (2 us) and the join.
 #include "kda_enqueue.h"
@@ -53,7 +53,7 @@ constexpr int min_tiles(int KB) { return setup_of(KB) + 1; }
 // for 32; at 64 units, 64 sequences of 64 heads, it would cost: 117 for 106).
 constexpr int FEW_UNITS = 64, JOIN_SHARES = 16;
 // Units are of 64 rows where that leaves a run this many tiles: each is read from LDS
-// and from memory half as often (2,048 new tokens 3.1 ms for 4.6, 24 sequences of some 4
+// and from memory half as often (2,048 new tokens 3.0 ms for 4.6, 24 sequences of some 4
 // tokens 97 us for 108, 256
 // sequences of 1,000 rows and 128 heads 166 for 225).  With fewer tiles the shorter turns of
 // 32 rows, in more runs, win (four sequences of 8,000 rows, 128 heads: 40 us for 50).
@@ -263,8 +263,7 @@ struct Attend {
     for (int k = 0; k < S::KT; ++k)
 #pragma unroll
       for (int i = 0; i < 4; ++i) mx = fmaxf(mx, sc[k][i]);
-    mx = fmaxf(mx, __shfl_xor(mx, 16));
-    mx = fmaxf(mx, __shfl_xor(mx, 32));
+    mx = max_halves(max_sixteens(mx));
     x.tops[kg][row] = mx;  // (four lanes the same)
     if (!SAFE) x.odd[wave] = odd;
     exchanged();
@@ -304,6 +303,10 @@ struct Attend {
     if (!SAFE && __builtin_expect(not_whole, 0)) {
       if (__any(x.odd[lane % S::NW])) return false;
     }
+    const auto value = [&](int i) { return value_frags.load(tile, 16 * (i / S::NV), i % S::NV); };
+    F first[2];  // (read while the others come: 3.05 -> 3.01 ms)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) first[i] = value(i);
     exchanged();
 
     const auto weight = [&](int v, int k) {
@@ -322,16 +325,18 @@ struct Attend {
     F p[2][S::RV];
 #pragma unroll
     for (int v = 0; v < S::RV; ++v) p[0][v] = weight(v, 0);
-    pipelined<F, KB / 16 * S::NV, 2>([&](int i) { return value_frags.load(tile, 16 * (i / S::NV), i % S::NV); },
-                                     [&](int i, F val) {
-                                       const int k = i / S::NV, d = i % S::NV;
-                                       if (d == 0 && k + 1 < KB / 16) {
+    pipelined_from<F, KB / 16 * S::NV, 2>(
+        first, value,
+        [&](int i, F val) {
+          const int k = i / S::NV, d = i % S::NV;
+          if (d == 0 && k + 1 < KB / 16) {
 #pragma unroll
-                                         for (int v = 0; v < S::RV; ++v) p[(k + 1) % 2][v] = weight(v, k + 1);
-                                       }
+            for (int v = 0; v < S::RV; ++v) p[(k + 1) % 2][v] = weight(v, k + 1);
+          }
 #pragma unroll
-                                       for (int v = 0; v < S::RV; ++v) o[d][v] = mma16(val, p[k % 2][v], o[d][v]);
-                                     });
+          for (int v = 0; v < S::RV; ++v) o[d][v] = mma16(val, p[k % 2][v], o[d][v]);
+        },
+        [](int) {});
     return true;
   }
 

@@ -131,11 +131,10 @@ struct ColFrags {
 // read while the group before runs.  (Left to itself the compiler reads each operand
 // right before its step, where registers are short.)  load(i) answers step i's operand,
 // step(i, operand) runs it, and between(g) is other work for behind group g's steps.
+// `now` holds the first group's operands.
 template <typename F, int N, int G, typename Load, typename Step, typename Between>
-__device__ __forceinline__ void pipelined(Load load, Step step, Between between) {
-  F now[G], next[G];
-#pragma unroll
-  for (int i = 0; i < G; ++i) now[i] = load(i);
+__device__ __forceinline__ void pipelined_from(F (&now)[G], Load load, Step step, Between between) {
+  F next[G];
 #pragma unroll
   for (int g = 0; g < N; g += G) {
 #pragma unroll
@@ -150,6 +149,13 @@ __device__ __forceinline__ void pipelined(Load load, Step step, Between between)
 #pragma unroll
     for (int i = 0; i < G; ++i) now[i] = next[i];
   }
+}
+template <typename F, int N, int G, typename Load, typename Step, typename Between>
+__device__ __forceinline__ void pipelined(Load load, Step step, Between between) {
+  F now[G];
+#pragma unroll
+  for (int i = 0; i < G; ++i) now[i] = load(i);
+  pipelined_from<F, N, G>(now, load, step, between);
 }
 template <typename F, int N, int G, typename Load, typename Step>
 __device__ __forceinline__ void pipelined(Load load, Step step) {
@@ -223,6 +229,19 @@ __device__ __forceinline__ void fetched() {
 
 // Values of the other half of the wave (lane l ^ 32).
 __device__ __forceinline__ float other_half(float x) { return __shfl_xor(x, 32); }
+
+// The larger of the values of lanes l and l ^ 32, l and l ^ 16, in both.  (The swaps exchange the
+// halves, or neighbouring sixteens, of two registers, without the way through LDS that a shuffle
+// takes.)
+__device__ __forceinline__ float larger_of(__attribute__((ext_vector_type(2))) unsigned x) {
+  return fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1]));
+}
+__device__ __forceinline__ float max_halves(float x) {
+  return larger_of(__builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false));
+}
+__device__ __forceinline__ float max_sixteens(float x) {
+  return larger_of(__builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false));
+}
 
 // The wave of this thread in its workgroup, as a scalar.
 __device__ __forceinline__ int wave_index() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }

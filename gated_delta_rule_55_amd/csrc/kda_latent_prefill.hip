@@ -101,7 +101,7 @@ struct Prefill {
     for (int t = 0; t < 2; ++t)
 #pragma unroll
       for (int i = 0; i < 16; ++i) top = fmaxf(top, s[t][i]);
-    top = fmaxf(top, other_half(top));
+    top = max_halves(top);
     // (a maximum's product with c is rounded the same way each time it is formed)
     const float base = top == -__builtin_inff() ? 0.f : __fmul_rn(top, c);
     const float alpha = fast_exp2(__fmul_rn(m, c) - base);
