@@ -1,7 +1,7 @@
-// kda_latent_torch.cpp -- the Python module _fast_latent: the calls of latent.py that
-// serve single tokens, without Python between the tensors and the C ABI, as
-// kda_torch.cpp has them for layer.py (a call after the other: 64 tokens' rotation 4.4 us and 9.3 through
-// Python, their append 3.9 and 11.3).
+// kda_latent_torch.cpp -- the Python module _fast_latent: the common calls of latent.py
+// without Python between the tensors and the C ABI, as kda_torch.cpp has them for
+// layer.py (one after the other: 64 tokens' rotation 4.4 us and 9.3 through Python, their
+// append 3.9 and 11.3).
 //
 // Every function takes all its arguments by position and returns what the entry point
 // returns, or None for any call it does not take: latent.py then makes the call itself,
@@ -72,6 +72,87 @@ bool pages(Args& a, Desc& d, int64_t& W, PyObject* cache, PyObject* table, PyObj
   return a.ok = a.ok && (cu != Py_None || T == N);
 }
 
+// A call's workspace: the caller's tensor, or a new one of the bytes that need(&status) answers.
+struct Workspace {
+  void* p = nullptr;
+  size_t bytes = 0;
+  at::Tensor made;
+
+  template <typename Need>
+  bool take(Args& a, PyObject* given, Need need) {
+    if (given != Py_None) {
+      const at::Tensor* t = a.tensor(given);
+      if (!t || t->device().index() != a.dev) return a.ok = false;
+      p = t->data_ptr();
+      bytes = (size_t)t->nbytes();
+      return true;
+    }
+    int status = KDA_OK;
+    bytes = need(&status);
+    if (status != KDA_OK) return a.ok = false;
+    if (bytes) {
+      made = a.empty({(int64_t)bytes}, at::kByte);
+      p = made.data_ptr();
+    }
+    return true;
+  }
+};
+
+// (q, k, k_pe, v, cu_seqlens, cu_seqlens_k, scale, out, workspace)
+PyObject* latent_prefill(PyObject*, PyObject* const* p, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    Args a;
+    View q, k, pe, v;
+    if (n != 9 || !first(a, p[0]) || !q.read(a, p[0], 3) || !q.dense_heads() || !k.read(a, p[1], 3) ||
+        !pe.read(a, p[2], 2) || !v.read(a, p[3], 3))
+      Py_RETURN_NONE;
+    const int64_t T = q.rows, K = k.rows, H = q.heads;
+    if (!k.is(K, H, k.d) || !v.is(K, H, v.d) || !pe.is(K, 1, q.d - k.d)) Py_RETURN_NONE;
+    kda_latent_prefill_desc d{};
+    d.struct_size = sizeof(d);
+    d.dtype = type_of(a.dt);
+    d.n_seqs = 1;
+    if (p[4] != Py_None) {
+      const at::Tensor* cu = a.tensor(p[4]);
+      if (!cu || cu->dim() != 1 || cu->size(0) < 1 || cu->size(0) > INT32_MAX) Py_RETURN_NONE;
+      d.n_seqs = (int32_t)(cu->size(0) - 1);
+      d.cu_seqlens = static_cast<const int32_t*>(a.ptr(p[4], at::kInt, {cu->size(0)}));
+    }
+    if (p[5] != Py_None) {
+      if (p[4] == Py_None) Py_RETURN_NONE;
+      d.cu_seqlens_k = static_cast<const int32_t*>(a.ptr(p[5], at::kInt, {(int64_t)d.n_seqs + 1}));
+    } else if (K != T) {
+      Py_RETURN_NONE;
+    }
+    if (p[6] != Py_None) {
+      d.scale = a.number(p[6]);
+      if (d.scale == 0.f) Py_RETURN_NONE;  // which stands for the default
+    }
+    d.n_heads = (int32_t)H;
+    d.dn = (int32_t)k.d, d.dr = (int32_t)pe.d, d.dv = (int32_t)v.d;
+    d.q_total = T, d.k_total = K;
+    d.q = q.p, d.k = k.p, d.k_pe = pe.p, d.v = v.p;
+    d.q_stride = q.row, d.k_stride = k.row, d.k_head_stride = k.head, d.k_pe_stride = pe.row;
+    d.v_stride = v.row, d.v_head_stride = v.head;
+    at::Tensor out;
+    if (p[7] == Py_None) {
+      d.o = a.output(p[7], a.dt, {T, H, v.d}, out);
+    } else {
+      View o;
+      if (!o.read(a, p[7], 3) || !o.is(T, H, v.d) || !o.dense_heads()) Py_RETURN_NONE;
+      d.o = o.p;
+      d.o_stride = o.row;
+    }
+    if (!a.ok) Py_RETURN_NONE;
+    Workspace ws;
+    if (!ws.take(a, p[8], [&](int* status) { return kda_latent_prefill_workspace_bytes(&d, status); })) Py_RETURN_NONE;
+    Ref result = wrap(p[7], out);
+    if (!result.p) return nullptr;
+    void* const stream = a.stream();
+    return answer(unlocked([&] { return kda_latent_prefill(&d, ws.p, ws.bytes, stream); }), "kda_latent_prefill", result);
+  });
+}
+
 // (q, cache, block_table, seq_lens, cu_seqlens, latent_dim, scale, out, workspace)
 PyObject* latent_attend(PyObject*, PyObject* const* p, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
@@ -93,7 +174,7 @@ PyObject* latent_attend(PyObject*, PyObject* const* p, Py_ssize_t n) {
     d.scale = a.number(p[6]);
     d.q = q.p;
     d.q_stride = q.row;
-    at::Tensor out, made;
+    at::Tensor out;
     if (p[7] == Py_None) {
       d.o = a.output(p[7], a.dt, {q.rows, q.heads, dc}, out);
     } else {
@@ -103,26 +184,12 @@ PyObject* latent_attend(PyObject*, PyObject* const* p, Py_ssize_t n) {
       d.o_stride = o.row;
     }
     if (!a.ok) Py_RETURN_NONE;
-    void* ws = nullptr;
-    size_t bytes = 0;
-    if (p[8] != Py_None) {
-      const at::Tensor* t = a.tensor(p[8]);
-      if (!t || t->device().index() != a.dev) Py_RETURN_NONE;
-      ws = t->data_ptr();
-      bytes = (size_t)t->nbytes();
-    } else {
-      int status = KDA_OK;
-      bytes = kda_latent_workspace_bytes(&d, &status);
-      if (status != KDA_OK) Py_RETURN_NONE;
-      if (bytes) {
-        made = a.empty({(int64_t)bytes}, at::kByte);
-        ws = made.data_ptr();
-      }
-    }
+    Workspace ws;
+    if (!ws.take(a, p[8], [&](int* status) { return kda_latent_workspace_bytes(&d, status); })) Py_RETURN_NONE;
     Ref result = wrap(p[7], out);
     if (!result.p) return nullptr;
     void* const stream = a.stream();
-    return answer(unlocked([&] { return kda_latent_attend(&d, ws, bytes, stream); }), "kda_latent_attend", result);
+    return answer(unlocked([&] { return kda_latent_attend(&d, ws.p, ws.bytes, stream); }), "kda_latent_attend", result);
   });
 }
 
@@ -207,6 +274,7 @@ PyObject* rotary(PyObject*, PyObject* const* p, Py_ssize_t n) {
 }
 
 PyMethodDef kMethods[] = {
+    {"latent_prefill", (PyCFunction)(void (*)(void))latent_prefill, METH_FASTCALL, nullptr},
     {"latent_attend", (PyCFunction)(void (*)(void))latent_attend, METH_FASTCALL, nullptr},
     {"latent_append", (PyCFunction)(void (*)(void))latent_append, METH_FASTCALL, nullptr},
     {"rotary", (PyCFunction)(void (*)(void))rotary, METH_FASTCALL, nullptr},

@@ -19,11 +19,10 @@ page of the cache (past the table, or a page number outside it) is neither
 written nor seen.
 
 Calls run on the device of their tensors, on `stream` or that device's current
-stream; outputs and workspaces made here are allocated for that stream.  All but
-latent_prefill go through the module _fast_latent (csrc/kda_latent_torch.cpp) where
-the device is the current one and no stream is named; it answers None to every call
-that it does not take or would have to refuse, which is then checked here, and made or
-refused.
+stream; outputs and workspaces made here are allocated for that stream.  Calls go
+through the module _fast_latent (csrc/kda_latent_torch.cpp) where the device is the
+current one and no stream is named; it answers None to every call that it does not
+take or would have to refuse, which is then checked here, and made or refused.
 """
 from __future__ import annotations
 
@@ -163,6 +162,10 @@ def latent_prefill(q: torch.Tensor, k: torch.Tensor, k_pe: torch.Tensor, v: torc
     do not ascend from 0 give unspecified results but no access out of bounds.
     Rows of out outside every sequence are left as they were.  workspace: a buffer of
     latent_prefill_workspace_bytes bytes (often 0), as in latent_decode."""
+    if _fast_latent is not None and stream is None:
+        done = _fast_latent.latent_prefill(q, k, k_pe, v, cu_seqlens, cu_seqlens_k, scale, out, workspace)
+        if done is not None:
+            return done
     dev, dt = _common("latent_prefill", q, "q", 3)
     for t, name in ((k, "k"), (v, "v")):
         if not isinstance(t, torch.Tensor) or t.dim() != 3:

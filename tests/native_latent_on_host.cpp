@@ -50,6 +50,14 @@ size_t kda_latent_workspace_bytes(const kda_latent_attend_desc*, int* status) {
   *status = KDA_OK;
   return 64;
 }
+int kda_latent_prefill(const kda_latent_prefill_desc* d, void*, size_t bytes, void*) {
+  g_workspace = bytes;
+  return answer(d);
+}
+size_t kda_latent_prefill_workspace_bytes(const kda_latent_prefill_desc* d, int* status) {
+  *status = d->dn == 8 ? KDA_ERR_UNSUPPORTED : KDA_OK;
+  return d->k_total == d->q_total ? 0 : 32;
+}
 int kda_latent_append(const kda_latent_append_desc* d, void*) { return answer(d); }
 int kda_rotary(const kda_rotary_desc* d, void*) { return answer(d); }
 

@@ -243,7 +243,10 @@ def test_the_native_module_and_ctypes_make_the_same_call(kda, dtype, monkeypatch
     def run():
         c = cache.clone()
         kda.latent_append(c, row[:, :256], row[:, 256:], table, lens, weight=torch.ones(256, device="cuda"), frequencies=f)
-        return [c, kda.rotary(x[..., 64:], lens, f, interleaved=True), kda.latent_decode(q, c, table, lens, 256, 0.1),
+        kv, pe = torch.cat([x, x[..., :32]], 2), x[:, 0, :32]
+        return [c, kda.latent_prefill(x, kv[..., :64], pe, kv[..., 64:]),
+                kda.latent_prefill(x, kv[..., :64], pe, kv[..., 64:], ints([0, 1, 2]), ints([0, 0, 2]), scale=0.3),
+                kda.rotary(x[..., 64:], lens, f, interleaved=True), kda.latent_decode(q, c, table, lens, 256, 0.1),
                 kda.latent_extend(q, c, table, lens, ints([0, 1, 2]), 256, 0.1)]
 
     def refusals():
@@ -254,6 +257,9 @@ def test_the_native_module_and_ctypes_make_the_same_call(kda, dtype, monkeypatch
                      lambda: kda.latent_extend(q, cache, table, lens, None, 256, 0.1),
                      lambda: kda.latent_append(cache, row[:, :256], row[:, 256:], table, lens, eps=-1.0),
                      lambda: kda.latent_append(cache, row[:, :240], row[:, 240:], table, lens),
+                     lambda: kda.latent_prefill(x, x[..., :64], x[:, 0, 64:], x[..., :48]),
+                     lambda: kda.latent_prefill(x, x[..., :64], x[:, 0, 64:], x[..., :64], scale=0.0),
+                     lambda: kda.latent_prefill(x, x[..., :64], x[:, 0, 64:], x[..., :64], None, ints([0, 2])),
                      lambda: kda.rotary(x[..., 64:], lens, f[:8]),
                      lambda: kda.rotary(x[..., 2:34], lens, f),
                      lambda: kda.rotary(x[..., 64:], lens, f, magnitude=0.0)):
@@ -261,11 +267,11 @@ def test_the_native_module_and_ctypes_make_the_same_call(kda, dtype, monkeypatch
                 make()
 
     calls = []
-    for name in ("latent_attend", "latent_append", "rotary"):
+    for name in ("latent_prefill", "latent_attend", "latent_append", "rotary"):
         real = getattr(latent._fast_latent, name)
         monkeypatch.setattr(latent._fast_latent, name, lambda *a, real=real: calls.append(real(*a)) or calls[-1])
     native = run()
-    assert len(calls) == 4 and all(c is not None for c in calls)
+    assert len(calls) == 6 and all(c is not None for c in calls)
     refusals()
     monkeypatch.setattr(latent, "_fast_latent", None)
     for a, b in zip(native, run()):

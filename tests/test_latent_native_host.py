@@ -20,7 +20,7 @@ pytestmark = pytest.mark.skipif(
     not (shutil.which("g++") and os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h"))),
     reason="needs g++ and Python's headers")
 
-DESC = {"latent_attend": al.LatentAttendDesc, "latent_append": al.LatentAppendDesc, "rotary": al.RotaryDesc}
+DESC = {"latent_prefill": al.LatentPrefillDesc, "latent_attend": al.LatentAttendDesc, "latent_append": al.LatentAppendDesc, "rotary": al.RotaryDesc}
 
 
 @pytest.fixture(scope="module")
@@ -69,7 +69,16 @@ def rotary(x=None, positions=LENS, freq=FREQ, interleaved=True, magnitude=1.0, o
     return "rotary", (torch.zeros(3, 2, 64) if x is None else x, positions, freq, interleaved, magnitude, out)
 
 
-CALLS = [attend(), attend(cu=i32(0, 1, 1, 3), out=torch.zeros(3, 2, 256)), append(), append(weight=None, freq=None),
+KV = torch.zeros(5, 2, 192)
+CU, CUK = i32(0, 1, 3), i32(0, 4, 5)
+
+
+def prefill(q=None, k=KV[..., :64], pe=torch.zeros(5, 32), v=KV[..., 64:], cu=CU, cuk=CUK, scale=None, out=None,
+            workspace=None):
+    return "latent_prefill", (torch.zeros(3, 2, 96) if q is None else q, k, pe, v, cu, cuk, scale, out, workspace)
+
+
+CALLS = [prefill(), prefill(scale=0.5, out=torch.zeros(3, 2, 128)), attend(), attend(cu=i32(0, 1, 1, 3), out=torch.zeros(3, 2, 256)), append(), append(weight=None, freq=None),
          rotary(), rotary(out=torch.zeros(3, 2, 64))]
 IDS = [f"{n}-{i % 2}" for i, (n, _) in enumerate(CALLS)]
 
@@ -108,8 +117,8 @@ def test_the_wrapper_passes_the_error_on(fast, monkeypatch):
     for name, a in CALLS:
         fast.host.host_reset(-7)
         with pytest.raises(KdaError):
-            if name == "latent_append":
-                latent.latent_append(*a)
+            if name in ("latent_append", "latent_prefill"):
+                getattr(latent, name)(*a)
             elif name == "rotary":
                 latent.rotary(*a)
             elif a[4] is None:
@@ -117,6 +126,25 @@ def test_the_wrapper_passes_the_error_on(fast, monkeypatch):
             else:
                 latent.latent_extend(*a)
         assert fast.host.host_calls() == 1
+
+
+def test_prefill_descriptor(fast):
+    wide, out, rows = torch.zeros(3, 3, 96)[:, 1:], torch.zeros(3, 4, 128)[:, :2], torch.zeros(5, 40)
+    d = seen(fast, prefill(q=wide, pe=rows[:, 8:], out=out, scale=0.25))
+    assert (d.n_seqs, d.n_heads, d.dn, d.dr, d.dv, d.q_total, d.k_total) == (2, 2, 64, 32, 128, 3, 5)
+    assert (d.q, d.q_stride, d.o, d.o_stride) == (wide.data_ptr(), 288, out.data_ptr(), 512)
+    assert (d.k, d.k_stride, d.k_head_stride) == (KV.data_ptr(), 384, 192)
+    assert (d.v, d.v_stride, d.v_head_stride) == (KV.data_ptr() + 256, 384, 192)
+    assert (d.k_pe, d.k_pe_stride) == (rows.data_ptr() + 32, 40)
+    assert (d.cu_seqlens, d.cu_seqlens_k, d.scale) == (CU.data_ptr(), CUK.data_ptr(), 0.25)
+    assert fast.host.host_workspace() == 32
+    d = seen(fast, prefill(q=torch.zeros(5, 2, 96), cu=None, cuk=None))
+    assert (d.n_seqs, d.cu_seqlens, d.cu_seqlens_k, d.scale) == (1, None, None, 0) and fast.host.host_workspace() == 0
+    d = seen(fast, prefill(q=torch.zeros(5, 2, 96), cuk=None))
+    assert (d.n_seqs, d.cu_seqlens, d.cu_seqlens_k) == (2, CU.data_ptr(), None)
+    assert run(fast, prefill()).shape == (3, 2, 128) and run(fast, prefill(out=out)) is out
+    run(fast, prefill(workspace=torch.zeros(7)))
+    assert fast.host.host_workspace() == 28
 
 
 def test_attend_descriptor(fast):
@@ -160,6 +188,14 @@ def test_rotary_descriptor(fast):
 
 
 NOT_TAKEN = [
+    prefill(q=torch.zeros(3, 2, 96).bfloat16()), prefill(q=torch.zeros(3, 2, 192)[..., :96]), prefill(q=torch.zeros(3, 1, 96)),
+    prefill(q=torch.zeros(3, 96)), prefill(k=KV[:4, :, :64]), prefill(v=KV[:4, :, 64:]), prefill(v=KV[:, :1, 64:]),
+    prefill(pe=torch.zeros(5, 64)), prefill(pe=torch.zeros(4, 32)), prefill(pe=torch.zeros(5, 2, 32)),
+    prefill(k=KV[:, :1].expand(5, 2, 192)[..., :64]), prefill(k=KV[..., :128:2]), prefill(cu=None), prefill(cuk=None),
+    prefill(cu=CU.long()), prefill(cu=CU[None]), prefill(cu=CU[:0]), prefill(cuk=i32(0, 5)), prefill(cuk=CUK.long()),
+    prefill(scale=0.0), prefill(scale=1e-60), prefill(scale="1"), prefill(out=torch.zeros(3, 2, 64)),
+    prefill(out=torch.zeros(3, 2, 256)[..., :128]), prefill(workspace=3), prefill(workspace=torch.zeros(4, 4)[:, :2]),
+    prefill(k=torch.zeros(5, 2, 8), pe=torch.zeros(5, 88)),   # the library names no workspace
     attend(q=torch.zeros(3, 2, 320, dtype=torch.float16)), attend(q=torch.zeros(3, 2, 640)[..., ::2]),
     attend(q=torch.zeros(3, 2, 640)[..., :320]), attend(q=torch.zeros(320, 3, 2).permute(1, 2, 0)),
     attend(q=torch.zeros(1, 2, 320).expand(3, 2, 320)), attend(q=torch.zeros(4, 2, 320)),
@@ -187,7 +223,7 @@ def test_a_call_that_it_does_not_take_is_handed_back(fast, call):
     assert run(fast, call) is None and fast.host.host_calls() == 0
 
 
-@pytest.mark.parametrize("call", [attend(), append(), rotary()], ids=["attend", "append", "rotary"])
+@pytest.mark.parametrize("call", [prefill(), attend(), append(), rotary()], ids=["prefill", "attend", "append", "rotary"])
 def test_numbers_of_arguments(fast, call):
     fast.host.host_reset(0)
     f, a = getattr(fast, call[0]), call[1]
@@ -197,6 +233,7 @@ def test_numbers_of_arguments(fast, call):
 def test_no_rows(fast):
     """Nothing to do is taken too: the library says so."""
     none = torch.zeros(0, dtype=torch.int32)
+    assert run(fast, prefill(q=torch.zeros(0, 2, 96))).shape == (0, 2, 128)
     assert run(fast, attend(q=torch.zeros(0, 2, 320), table=TABLE[:0], lens=none)).shape == (0, 2, 256)
     assert run(fast, append(latent=torch.zeros(0, 256), pe=torch.zeros(0, 64), table=TABLE[:0], lens=none)) is CACHE
     assert run(fast, rotary(x=torch.zeros(0, 2, 64), positions=none)).shape == (0, 2, 64)
