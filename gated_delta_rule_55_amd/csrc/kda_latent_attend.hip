@@ -54,7 +54,7 @@ constexpr int min_tiles(int KB) { return setup_of(KB) + 1; }
 constexpr int FEW_UNITS = 64, JOIN_SHARES = 16;
 // Units are of 64 rows where that leaves a run this many tiles: each is read from LDS
 // and from memory half as often (2,048 new tokens 3.0 ms for 4.6, 24 sequences of some 4
-// tokens 97 us for 108, 256
+// tokens 93 us for 108, 256
 // sequences of 1,000 rows and 128 heads 166 for 225).  With fewer tiles the shorter turns of
 // 32 rows, in more runs, win (four sequences of 8,000 rows, 128 heads: 40 us for 50).
 constexpr int LONG_RUN = 6;
@@ -425,6 +425,15 @@ __device__ __forceinline__ bool attend_piece(const LatentAttendArgs& a, const Wo
 
   A s_(lane, wave);
   look_up(tile0);
+  // LDS of the piece before is done with (where that stopped, a tile's fetches too)
+  if (SAFE)
+    fetched();
+  else
+    exchanged();
+  aim(tile0, x.have[0]);
+#pragma unroll
+  for (int b = 0; b < S::blocks; ++b) fetch(b, even);
+  // (the queries come while the rows do)
   const int kg = wave % S::KG, rg = wave / S::KG;
   {
     const int r = min(row0 + rg * 16 + col, n_rows - 1), tok = r / a.n_heads;
@@ -433,10 +442,6 @@ __device__ __forceinline__ bool attend_piece(const LatentAttendArgs& a, const Wo
 #pragma unroll
     for (int k = 0; k < S::KS; ++k) s_.q[k] = load_frag8<T>(qr + 32 * k + 8 * grp);
   }
-  fetched();  // LDS of the piece before is done with
-  aim(tile0, x.have[0]);
-#pragma unroll
-  for (int b = 0; b < S::blocks; ++b) fetch(b, even);
 #pragma unroll
   for (int v = 0; v < S::RV; ++v) s_.my_limit[v] = limit_of(32 * v + (lane & 31));
   // (behind the last tile rows that do not exist are fetched)
@@ -636,7 +641,7 @@ __global__ __launch_bounds__(JOIN_THREADS) void latent_join_kernel(LatentAttendA
 template <typename T, int DC, int DR, int R>
 hipError_t run(const LatentAttendArgs& a, const Plan& plan, const Workspace& ws, hipStream_t stream) {
   hipError_t e = enqueue(latent_attend_kernel<T, DC, DR, R>, (unsigned)plan.runs, Shape<T, DC, DR, R>::THREADS, stream, a, ws);
-  if (e != hipSuccess) return e;
+  if (e != hipSuccess || plan.runs == 1) return e;  // (a single run cuts no unit)
   constexpr int KB = Shape<T, DC, DR, R>::KB;
   if (plan.units <= FEW_UNITS / 8)  // their rows alone would not fill the GPU
     return enqueue(latent_join_kernel<T, DC, R, KB, 128>, (unsigned)(plan.heads * R * (DC / 128)), JOIN_THREADS, stream, a,
