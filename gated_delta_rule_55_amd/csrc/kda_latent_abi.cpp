@@ -282,10 +282,11 @@ int kda_latent_append(const kda_latent_append_desc* d, void* stream) {
   const RowSet lat = row_set(d->latent, T, a.latent_stride, d->dc, es), pe = row_set(d->k_pe, T, a.pe_stride, d->dr, es);
   const RowSet out = row_set(d->rows_out, T, a.rows_stride, W, es);
   const Range cache = cache_range(d->cache, g, W, es);
-  // rows_out may be where both inputs are, row for row
-  const bool in_place = d->rows_out && d->rows_out == d->latent && a.rows_stride == a.latent_stride &&
-                        a.rows_stride == a.pe_stride &&
-                        (const char*)d->k_pe == (const char*)d->latent + d->dc * es;
+  // rows_out may be where both inputs are, row for row (a single row has no stride: callers
+  // give any)
+  const bool in_place = d->rows_out && d->rows_out == d->latent &&
+                        (const char*)d->k_pe == (const char*)d->latent + d->dc * es &&
+                        (T == 1 || (a.rows_stride == a.latent_stride && a.rows_stride == a.pe_stride));
   if (!in_place && (overlap(out, lat) || overlap(out, pe))) return KDA_ERR_ALIAS;
   if (overlap(cache, range_of(lat)) || overlap(cache, range_of(pe)) || overlap(cache, range_of(out))) return KDA_ERR_ALIAS;
   const Range small[] = {tables[0], tables[1], tables[2], range_of(d->weight, d->weight ? (int64_t)d->dc * 4 : 0),
@@ -331,7 +332,7 @@ int kda_rotary(const kda_rotary_desc* d, void* stream) {
     return KDA_ERR_ALIGN;
   const RowSet x = head_rows(d->x, T, a.x_stride, H, a.x_head, d->dim, es);
   const RowSet y = head_rows(d->y, T, a.y_stride, H, a.y_head, d->dim, es);
-  const bool in_place = d->x == d->y && a.x_stride == a.y_stride && a.x_head == a.y_head;
+  const bool in_place = d->x == d->y && (T == 1 || a.x_stride == a.y_stride) && (H == 1 || a.x_head == a.y_head);
   if (!in_place && overlap(x, y)) return KDA_ERR_ALIAS;
   if (overlap(range_of(y), range_of(d->positions, T * 4)) ||
       overlap(range_of(y), range_of(d->frequencies, (int64_t)d->dim * 4)))

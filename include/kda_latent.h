@@ -151,7 +151,7 @@ typedef enum {
  * also receives each token's row where it is not NULL, also of tokens whose
  * position has no row in the cache.  Tokens outside every sequence are not
  * touched.  rows_out may be the buffer that latent and k_pe are slices of, at
- * the same places and strides.  Two tokens of one position (a page twice in the
+ * the same places and strides (one token: at any strides).  Two tokens of one position (a page twice in the
  * table) leave a mixture of their rows. */
 typedef struct {
   uint32_t struct_size;        /* sizeof(kda_latent_append_desc)                */
