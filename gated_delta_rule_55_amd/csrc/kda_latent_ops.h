@@ -249,7 +249,8 @@ __device__ __forceinline__ int wave_index() { return __builtin_amdgcn_readfirstl
 // A value that all lanes have, as a scalar.  What is read from LDS counts as different
 // in each lane otherwise, and a branch on it as one that lanes take by themselves: the
 // kernels here have none of those where registers are full, since copies that the
-// compiler makes behind such a branch, to free registers, have missed lanes.
+// compiler (AMD clang 22 of ROCm 7.2) makes behind such a branch, to free registers, have
+// missed lanes.  tests/test_latent_codegen_host.py looks for both in what it made.
 __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
 __device__ __forceinline__ int64_t uniform(int64_t x) {
   return (int64_t)((uint64_t)(uint32_t)uniform((int)(x >> 32)) << 32 | (uint32_t)uniform((int)x));
