@@ -22,9 +22,22 @@
 // 8,192 rows on average, 32 heads, 137 us, 4.4 TB/s of the 5.0 that a copy reaches.  Many queries a row:
 // a tile's turn takes 2.8 us at R = 64, of which the matrix instructions are 0.9, the
 // reads of LDS (each key by four waves) 1.4, and three barriers keep the two from
-// overlapping fully: 2,048 new tokens of 32 heads 3.0 ms, 0.82 PFLOP/s.  One
-// sequence: the start (tables, pages and first rows one after the other: 7 us), the end
-// of a piece (2 us) and the join.
+// overlapping fully: 2,048 new tokens of 32 heads on 18,432 rows 3.1 ms, 0.81 PFLOP/s.  A few
+// tokens a sequence: the rows' bytes again, but a sequence's two or three units take its rows at
+// different times on different XCDs, so that 24 sequences of 113 MB read 343 and write 60 of
+// pieces, at 4.7 TB/s.  One sequence of 32,768 rows, 28 us: a piece's start (tables, pages and
+// first rows one after the other) and end 11, four tiles of 1.9, the join and its launch 6, and 4
+// for what 128 workgroups at once have to wait for the memory.
+//
+// In bf16 the weights P are rounded before they meet the values (2^-8 of a weight at most), since
+// the matrix cores take operands of one type and fp32's run at an eighth of the rate; a second
+// product for the rest of each weight would double the work of O.  Their sum is taken before
+// that.  Against float64 the outputs' error grows from that of their own rounding, 1.7e-3 of
+// their norm, to 1.8e-3.
+//
+// Every unit counts as all of its sequence's rows where the tiles are shared out, though its
+// queries may see fewer: where the new tokens are most of the sequence, the runs of its first
+// units are done early (2,048 new tokens of 2,048 rows: the longest walks 128 tiles, the mean 66).
 #include "kda_enqueue.h"
 #include "kda_latent_launch.h"
 #include "kda_latent_ops.h"
@@ -39,8 +52,12 @@ constexpr int RUNS = 256;     // workgroups: their tiles in LDS leave room for o
 // rows 26 us with 1, 30 with 2, 41 with 3): each unit counts as that many more, in front, so
 // that a run that crosses from one into another has fewer tiles for it.
 constexpr int setup_of(int KB) { return KB == 64 ? 3 : 1; }
-// Tiles of a run at least: one with its setup.  (Two, bf16: one sequence of 1,000 rows 27
-// us for 25; 32,768 rows 30 both ways.)
+// Tiles of a run at least, a unit's setup among them where the run begins one; a run inside a unit
+// has this many of the unit's.  Half of these would give a short sequence more workgroups and a
+// long one more pieces to join.  bf16, 32 heads, one sequence, us for 4 / 2 / 1: 1,000 rows 24.0 /
+// 18.7 / 17.2, 8,192 rows 24.5 / 20.9 / 21.9, 32,768 rows 28.6 / 30.9 / 30.9, 131,072 rows and
+// batches of 8 and more sequences the same; 5: 1,000 rows 27 for 25, 32,768 rows 30 both ways.
+// fp32: three sequences of 200 rows 25.0 us, with 1 19.6.
 constexpr int min_tiles(int KB) { return setup_of(KB) + 1; }
 
 // The workspace.  A run has at most two pieces of units that are cut: one that begins
@@ -48,11 +65,15 @@ constexpr int min_tiles(int KB) { return setup_of(KB) + 1; }
 // latter's head says where the unit's other pieces are.  Heads are numbered by unit
 // where a call has few of them, so that the join has a workgroup for each row of these and
 // no idle ones (one sequence of 32,768 rows, 128 heads: 46 us, by run 69), else by run,
-// with 16 workgroups each, which idle where a run begins no unit that is cut.  Where even the
-// rows would not fill the GPU a workgroup takes 128 columns of one (32 heads: 28 us
-// for 32; at 64 units, 64 sequences of 64 heads, it would cost: 117 for 106).
+// with 16 workgroups each, which idle where a run begins no unit that is cut (by unit and by
+// run, us: 16 units 33.9 and 35.8, 64 sequences of 4,000 rows 75.3 and 77.0, of 300 rows 26.9 and
+// 29.2; 128 of 2,000 rows 82.3 and 84.2, 256 of 1,000 rows 68.8 and 67.8).  Where even the
+// rows would not fill the GPU a workgroup takes 128 columns of one (columns by 128 and whole rows,
+// us: 1 unit 28.6 and 33.2, 8 units 32.4 and 33.5, 16 units 33.9 both ways, 32 units 45.7 and 43.9,
+// 64 units 80.9 and 75.0).
 constexpr int FEW_UNITS = 64, JOIN_SHARES = 16;
-// Units are of 64 rows where that leaves a run this many tiles: each is read from LDS
+// Units are of 64 rows where that leaves a run this many tiles, as far as the host can tell: lengths
+// are on the device, and each sequence counts as long as the table has places.  Each is read from LDS
 // and from memory half as often (2,048 new tokens 3.0 ms for 4.6, 24 sequences of some 4
 // tokens 93 us for 108, 256
 // sequences of 1,000 rows and 128 heads 166 for 225).  With fewer tiles the shorter turns of
@@ -285,7 +306,7 @@ struct Attend {
         for (int i = 0; i < 4; ++i) {
           const float e = fast_exp2(sc[k][i] * c - base);
           sum += e;
-          p[i] = from_f32<T>(e);  // bf16: one rounding, 2^-8
+          p[i] = from_f32<T>(e);  // bf16: one rounding, 2^-8 (see the top)
         }
         *reinterpret_cast<V4*>(weights + row * S::p_row + (key0 + 16 * k + 4 * grp) * ES) = p;
       }

@@ -13,8 +13,16 @@
 // LDS that bound it, not the memory.  Two tiles, one worked on while the other is
 // fetched straight into LDS, take 80 KB in bf16: two workgroups a CU, so that one's
 // softmax runs beside the other's products; fp32 takes 160 KB, one.  32,768 tokens, 32
-// heads of 128 + 64, bf16: 10.8 ms, 1.0 PFLOP/s where a large matrix product reaches 1.18; matrix
-// cores busy for 52 % of the cycles (the clock is at 1.8 GHz under this load), LDS for 43 %.
+// heads of 128 + 64, bf16: 10.8 to 11.2 ms on different cards, 0.98 to 1.02 PFLOP/s where a large
+// matrix product reaches 1.18; matrix cores busy for 52 % of the cycles (the clock is at 1.8 GHz
+// under this load), LDS for 43 %.  Waves of a block that have no query work along, on rows
+// that are not stored: a sequence of up to 32 queries costs the products of 128.
+//
+// In bf16 the weights are rounded before they meet the values (2^-8 of a weight at most), since the
+// matrix cores take operands of one type and fp32's run at an eighth of the rate; a second
+// product for the rest of each weight would be 40 % more of them.  Their sum is taken before
+// that.  Against float64 the outputs' error grows from that of their own rounding,
+// 1.6e-3 of their norm, to 1.9e-3.
 #include <algorithm>
 
 #include "kda_enqueue.h"
@@ -114,7 +122,7 @@ struct Prefill {
       for (int i = 0; i < 16; ++i) {
         const float x = fast_exp2(s[t][i] * c - base);
         sum += x;
-        p[2 * t + (i >> 3)][i & 7] = from_f32<T>(x);  // bf16: one rounding, 2^-8
+        p[2 * t + (i >> 3)][i & 7] = from_f32<T>(x);  // bf16: one rounding, 2^-8 (see the top)
       }
     l = l * alpha + sum;
     if (__builtin_expect(__any(alpha != 1.f), 0)) {

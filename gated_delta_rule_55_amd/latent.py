@@ -11,12 +11,16 @@ values and a positional part of dr.  Its serving path, call by call:
     latent_decode    one token per sequence, on the pages (absorbed queries)
     latent_extend    several new tokens per sequence, on the pages
 
-The last three share three tables with the first: block_table int32 [N, MP] (the
+The last two share three tables with the first: block_table int32 [N, MP] (the
 pages of each sequence), seq_lens int32 [N] (its rows, new tokens among them) and,
 where sequences have several new tokens, cu_seqlens int32 [N + 1].  All are read
 on the device, so a captured graph follows their contents; a position without a
 page of the cache (past the table, or a page number outside it) is neither
 written nor seen.
+
+Scores, softmax statistics and all sums are fp32.  In bf16 the softmax weights are rounded
+to bf16 before they multiply the values, as the matrix cores take them (2^-8 of a weight at
+most), and each output once more.
 
 Calls run on the device of their tensors, on `stream` or that device's current
 stream; outputs and workspaces made here are allocated for that stream.  Calls go
@@ -135,7 +139,8 @@ def _workspace(given, need, dev):
 
 def latent_prefill_workspace_bytes(T: int, K: int, H: int, nope_dim: int, rope_dim: int, value_dim: int,
                                    n_seqs: int = 1, dtype: torch.dtype = torch.bfloat16) -> int:
-    """Bytes of workspace latent_prefill needs for T queries and K keys in n_seqs sequences."""
+    """Bytes of workspace latent_prefill needs for T queries and K keys in n_seqs sequences.  Not
+    monotonic in these: a buffer for several sizes takes their maximum."""
     return _an.latent_prefill_workspace_bytes(_an.make(
         _an.LatentPrefillDesc, dtype=_DTYPES[dtype], n_seqs=n_seqs, n_heads=H, dn=nope_dim, dr=rope_dim,
         dv=value_dim, q_total=T, k_total=K, cu_seqlens_k=None if T == K else 16))
@@ -150,7 +155,7 @@ def latent_prefill(q: torch.Tensor, k: torch.Tensor, k_pe: torch.Tensor, v: torc
 
     q: [T, H, dn + dr]; k: [K, H, dn]; k_pe: [K, dr], shared by the heads; v:
     [K, H, dv]; dn and dv 64 or 128, dr 32 or 64; fp32 or bf16.  cu_seqlens: int32
-    [N + 1] on the device or None (one sequence).  cu_seqlens_k: the sequences'
+    [N + 1] on the device, N at least 1, or None (one sequence).  cu_seqlens_k: the sequences'
     keys where they have more (or fewer) of them than queries, as in the end of a
     prompt whose beginning is expanded too: the last query stands beside the last
     key, and a query before the first key has output 0.  scale: (dn + dr)^-1/2 by
@@ -226,7 +231,8 @@ def _pages(cache, dev, dt):
 
 def latent_workspace_bytes(T: int, H: int, latent_dim: int, rope_dim: int, n_seqs: int, max_pages: int,
                            page_size: int, dtype: torch.dtype = torch.bfloat16, extend: bool = False) -> int:
-    """Bytes of workspace latent_decode (extend: latent_extend) needs for these sizes."""
+    """Bytes of workspace latent_decode (extend: latent_extend) needs for these sizes.  Not monotonic
+    in these: a buffer for several sizes takes their maximum."""
     return _an.latent_workspace_bytes(_an.make(
         _an.LatentAttendDesc, dtype=_DTYPES[dtype], n_seqs=n_seqs, n_heads=H, dc=latent_dim, dr=rope_dim,
         page_size=page_size, max_pages=max_pages, scale=1.0, t_total=T, cu_seqlens=16 if extend else None))
@@ -280,7 +286,8 @@ def latent_decode(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tenso
     rows be wider (strides are multiples of 16 bytes).  workspace: a buffer of
     latent_workspace_bytes bytes, one for each call that may overlap another (a
     captured graph keeps its own); allocated here when None.  Rounding depends on
-    all sequences' lengths, which decide where the rows are shared out."""
+    all sequences' lengths, which decide where the rows are shared out.  The host knows MP alone, not
+    the lengths: a table much wider than they are can cost time, never a result."""
     return _attend("latent_decode", q, cache, block_table, seq_lens, None, latent_dim, scale, out, workspace, stream)
 
 
@@ -375,7 +382,7 @@ def rotary(x: torch.Tensor, positions: torch.Tensor, frequencies: torch.Tensor, 
     (x[2 i], x[2 i + 1]) where interleaved.  positions: int32 [T]; frequencies: fp64
     [dim / 2] (rotary_frequencies).  out may be x itself, or a slice of another
     buffer (the positional part of the absorbed queries).  Angles are formed in
-    fp64: far positions lose nothing."""
+    fp64, so far positions lose nothing; sine and cosine are fp32."""
     if _fast_latent is not None and stream is None:
         done = _fast_latent.rotary(x, positions, frequencies, interleaved, magnitude, out)
         if done is not None:
@@ -409,7 +416,8 @@ def rotary_frequencies(dim: int, base: float = 10000.0, factor: float = 1.0,
     frequency is divided by the factor (positions are interpolated).  With it, by
     parts: a pair that turns fewer than `slow` times over original_length positions
     is divided, one that turns more than `fast` times is kept, and between them the
-    two are mixed in proportion to the turns."""
+    two are mixed in proportion to the turns (some models mix in proportion to i
+    instead: such frequencies are the caller's to make)."""
     if dim < 2 or dim % 2:
         raise ValueError(f"dim must be even and positive, got {dim}")
     if not (base > 0 and factor > 0 and fast > slow >= 0) or (original_length is not None and original_length <= 0):

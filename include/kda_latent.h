@@ -22,7 +22,7 @@
  * Conventions are those of kda.h (struct_size first, device pointers owned by
  * the caller, every check on the host before anything is enqueued, no
  * allocation, no synchronisation, calls re-entrant).  Strides are in elements,
- * multiples of 16 bytes and at most 2^28; 0 = dense.  Alignment: 16 bytes for
+ * multiples of 16 bytes and at most 2^28 (between pages 2^40); 0 = dense.  Alignment: 16 bytes for
  * tensors of dtype, 8 for frequencies, 4 for weights and index tables.  An
  * output overlaps no input, unless a descriptor says otherwise.
  *
@@ -36,8 +36,8 @@
  *
  * Numerics: scores, softmax maxima and sums and all products' sums are fp32.
  * With bf16 inputs the softmax weights are rounded to bf16 (relative 2^-8 at
- * most, after their sum is taken) before they multiply the values; with fp32
- * inputs everything is fp32.  A query that sees no key has output 0.  NaN and
+ * most, after their sum is taken) before they multiply the values, which the
+ * matrix cores take in one type; with fp32 inputs everything is fp32.  A query that sees no key has output 0.  NaN and
  * infinities in rows that a query does not see do not reach its output; in rows
  * that it sees they do, an infinite value possibly as NaN.
  */
@@ -65,7 +65,7 @@ extern "C" {
 typedef struct {
   uint32_t struct_size;        /* sizeof(kda_latent_prefill_desc)               */
   int32_t dtype;               /* kda_dtype of q, k, k_pe, v, o                 */
-  int32_t n_seqs;              /* N >= 1                                        */
+  int32_t n_seqs;              /* N >= 1 (a batch of none is no call)           */
   int32_t n_heads;             /* H, 1 .. 65535                                 */
   int32_t dn, dr, dv;          /* dn and dv 64 or 128, dr 32 or 64              */
   float scale;                 /* 2^-126 .. 2^127; 0 = (dn + dr)^-1/2           */
@@ -82,7 +82,8 @@ typedef struct {
 
 /* Bytes of device workspace kda_latent_prefill needs: 0 but where the blocks of
  * queries are too few for the GPU and their keys are shared out (depends on sizes
- * only: dtype, n_seqs, n_heads, dn, dr, dv, q_total and k_total).  *status (host, may
+ * only: dtype, n_seqs, n_heads, dn, dr, dv, q_total and k_total; not monotonic in
+ * them, so a buffer for several calls has the largest of their sizes).  *status (host, may
  * be NULL) receives the kda_status of the check; 0 is returned when it fails. */
 size_t kda_latent_prefill_workspace_bytes(const kda_latent_prefill_desc* d, int* status);
 
@@ -102,7 +103,10 @@ int kda_latent_prefill(const kda_latent_prefill_desc* d, void* workspace, size_t
  *
  * A query's result depends, bit for bit, on the whole call: the rows are shared
  * out evenly over the GPU, and where a sequence's rows are cut depends on the
- * others' lengths. */
+ * others' lengths.  How many queries share a workgroup (32 or 64) is chosen by
+ * sizes alone, with max_pages * page_size for the sequences' lengths: a
+ * table much wider than they are can cost time (a quarter, for four sequences of
+ * 8,000 rows and 128 heads), never a result. */
 typedef struct {
   uint32_t struct_size;        /* sizeof(kda_latent_attend_desc)                */
   int32_t dtype;               /* kda_dtype of q, cache, o                      */
@@ -125,7 +129,8 @@ typedef struct {
 
 /* Bytes of device workspace kda_latent_attend needs (depends on sizes only:
  * dtype, n_seqs, n_heads, dc, dr, max_pages, page_size, t_total and whether
- * cu_seqlens is NULL).  *status (host, may be NULL) receives the kda_status of
+ * cu_seqlens is NULL; not monotonic in them, so a buffer for several calls has the
+ * largest of their sizes).  *status (host, may be NULL) receives the kda_status of
  * the check; 0 is returned when it fails. */
 size_t kda_latent_workspace_bytes(const kda_latent_attend_desc* d, int* status);
 
@@ -181,7 +186,8 @@ int kda_latent_append(const kda_latent_append_desc* d, void* stream);
 /* y = the rows of x turned by their token's position.  x, y [t_total, H, dim]
  * with token and head strides (a slice of wider heads); y may be x itself.  The
  * angle is formed in fp64 and reduced to one turn before its sine and cosine
- * are taken in fp32, so far positions cost no accuracy. */
+ * are taken in fp32 (off by at most 4 half steps of 1), so far positions cost no
+ * accuracy. */
 typedef struct {
   uint32_t struct_size;        /* sizeof(kda_rotary_desc)                       */
   int32_t dtype;               /* kda_dtype of x, y                             */
