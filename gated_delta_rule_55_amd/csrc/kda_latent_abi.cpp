@@ -65,6 +65,21 @@ RowSet head_rows(const void* p, int64_t rows, int64_t stride, int64_t heads, int
   return row_set(p, rows, stride, (heads - 1) * head_stride + d, es);
 }
 
+// Whether two sets of heads at the same strides share a byte: rows r apart and heads k apart do
+// where |by - r stride - k head| < d.  A row ends before the next begins, and a head too, so two
+// values of each can.  (Bytes.)
+bool heads_overlap(const void* x, const void* y, int64_t rows, int64_t stride, int64_t heads, int64_t head, int64_t d) {
+  const int64_t by = (int64_t)((uintptr_t)y - (uintptr_t)x);
+  const auto below = [](int64_t a, int64_t b) { return a / b - (a % b < 0 ? 1 : 0); };
+  for (int64_t r = below(by, stride), i = 0; i < 2; ++i, ++r) {
+    if (r <= -rows || r >= rows) continue;
+    const int64_t rest = by - r * stride;
+    for (int64_t k = below(rest, head), j = 0; j < 2; ++j, ++k)
+      if (k > -heads && k < heads && rest - k * head < d && k * head - rest < d) return true;
+  }
+  return false;
+}
+
 int check_pages(int32_t dtype, int32_t n_seqs, int32_t dc, int32_t dr, int32_t page_size, int32_t max_pages,
                 int32_t n_pages, int64_t page_stride, int64_t row_stride, int64_t t_total, bool cu, kda::LatentPages* g) {
   if (!dtype_ok(dtype)) return KDA_ERR_DTYPE;
@@ -332,8 +347,12 @@ int kda_rotary(const kda_rotary_desc* d, void* stream) {
     return KDA_ERR_ALIGN;
   const RowSet x = head_rows(d->x, T, a.x_stride, H, a.x_head, d->dim, es);
   const RowSet y = head_rows(d->y, T, a.y_stride, H, a.y_head, d->dim, es);
-  const bool in_place = d->x == d->y && (T == 1 || a.x_stride == a.y_stride) && (H == 1 || a.x_head == a.y_head);
-  if (!in_place && overlap(x, y)) return KDA_ERR_ALIAS;
+  // (a single row or head has no stride)
+  const bool alike = (T == 1 || a.x_stride == a.y_stride) && (H == 1 || a.x_head == a.y_head);
+  const bool in_place = d->x == d->y && alike;
+  if (!in_place && overlap(x, y) &&
+      (!alike || heads_overlap(d->x, d->y, T, a.x_stride * es, H, a.x_head * es, d->dim * es)))
+    return KDA_ERR_ALIAS;
   if (overlap(range_of(y), range_of(d->positions, T * 4)) ||
       overlap(range_of(y), range_of(d->frequencies, (int64_t)d->dim * 4)))
     return KDA_ERR_ALIAS;

@@ -184,7 +184,8 @@ typedef struct {
 int kda_latent_append(const kda_latent_append_desc* d, void* stream);
 
 /* y = the rows of x turned by their token's position.  x, y [t_total, H, dim]
- * with token and head strides (a slice of wider heads); y may be x itself.  The
+ * with token and head strides (a slice of wider heads); y may be x itself, or other
+ * columns of the same heads.  The
  * angle is formed in fp64 and reduced to one turn before its sine and cosine
  * are taken in fp32 (off by at most 4 half steps of 1), so far positions cost no
  * accuracy. */

@@ -83,3 +83,19 @@ def test_rotary_in_place(kda, way, dtype, tokens, heads):
     bound = 7 * F32 * np.concatenate([both, both], -1) + 1.01 * U[dtype] * np.abs(want)
     assert np.all(np.abs(host64(d[..., 128:]) - want) <= bound)
     assert torch.equal(d[..., :128].cpu(), q[..., :128])
+
+
+@pytest.mark.parametrize("dtype", [BF, torch.float32])
+@pytest.mark.parametrize("tokens", [1, 5])
+def test_rotary_into_other_columns(kda, way, dtype, tokens):
+    """From some columns of the heads into others, in rows that hold more than the heads."""
+    wide = normal(4, tokens, 4 * 192 + 576, dtype=dtype).cuda()
+    before, heads = wide.clone(), wide[:, :4 * 192].unflatten(1, (4, 192))
+    f, pos = 10000.0 ** (-np.arange(0, 64, 2) / 64), np.arange(tokens) + 9
+    x = host64(heads[..., 128:])
+    kda.rotary(heads[..., 128:], ints(pos), torch.from_numpy(f).cuda(), out=heads[..., 64:128])
+    want, both = oracle.rotary(x, pos, f, False), np.abs(x[..., :32]) + np.abs(x[..., 32:])
+    bound = 7 * F32 * np.concatenate([both, both], -1) + 1.01 * U[dtype] * np.abs(want)
+    assert np.all(np.abs(host64(heads[..., 64:128]) - want) <= bound)
+    heads[..., 64:128] = before[:, :4 * 192].unflatten(1, (4, 192))[..., 64:128]
+    assert torch.equal(wide, before)
