@@ -21,8 +21,8 @@
 // In bf16 the weights are rounded before they meet the values (2^-8 of a weight at most), since the
 // matrix cores take operands of one type and fp32's run at an eighth of the rate; a second
 // product for the rest of each weight is 40 % more of them and does not fit the registers (15.4 ms
-// for 10.9).  Their sum is taken before that.  Against float64 the outputs' error grows from that of their own rounding,
-// 1.6e-3 of their norm, to 1.9e-3.
+// for 10.9).  Their sum is taken before that.  Against float64 the outputs' error grows from that
+// of their own rounding, 1.6e-3 of their norm, to 1.9e-3.
 #include <algorithm>
 
 #include "kda_enqueue.h"
